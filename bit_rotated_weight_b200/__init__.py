@@ -14,6 +14,7 @@ codebook, two half-block scales, about 5 bits per weight.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -27,13 +28,17 @@ __all__ = [
     "tq4_1s_moe_workspace", "tq4_1s_moe", "tq4_1s_moe_logits", "tq4_1s_router_topk", "tq4_1s_moe_route", "tq4_1s_get_status", "tq4_1s_launch_count",
     "tq4_1s_linear_static", "tq4_1s_debug_hook", "Fp8Weight", "tq4_1s_to_fp8", "tq4_1s_linear_fp8",
     "AffineWeight", "tq4_1s_affine_quantize", "tq4_1s_affine_dequantize", "tq4_1s_affine_linear",
+    "tq4_1s_router_scored", "Int8Weight", "tq4_1s_int8_quantize", "tq4_1s_int8_dequantize",
+    "tq4_1s_linear_int8_workspace", "tq4_1s_linear_int8", "tq4_1s_moe_int8_workspace", "tq4_1s_moe_int8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtq4_1s.so")
 
 TQ_OK = 0
-TQ_DTYPE_F32, TQ_DTYPE_BF16 = 0, 1
+TQ_DTYPE_F32, TQ_DTYPE_BF16, TQ_DTYPE_F16 = 0, 1, 2
+TQ_SCORE_SOFTMAX, TQ_SCORE_SIGMOID = 0, 1
+TQ_GROUP_MAX, TQ_GROUP_TOP2 = 0, 1
 TQ_DEV_TIMEOUT, TQ_DEV_BAD_ROUTING, TQ_DEV_NONFINITE, TQ_DEV_SCALE_RANGE = 1, 2, 4, 8
 TQ_WEIGHT_STATIC = 1
 TQ_HOOK_FAIL_NEXT_CALLS, TQ_HOOK_WAIT_NS, TQ_HOOK_WITHHOLD_ARRIVAL = 1, 2, 3
@@ -57,6 +62,21 @@ class _AffineWeight(ctypes.Structure):
     _fields_ = [
         ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("bits", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("biases", ctypes.c_void_p),
+    ]
+
+
+class _Router(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32), ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class _Int8Weight(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("wscale", ctypes.c_void_p),
     ]
 
 
@@ -103,6 +123,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                 "tq4_1s_affine_dequantize": ([ctypes.POINTER(_AffineWeight), P, P], ctypes.c_int),
                 "tq4_1s_affine_linear_workspace": ([I64, ctypes.POINTER(_AffineWeight)], SZ),
                 "tq4_1s_affine_linear": ([P, I64, ctypes.POINTER(_AffineWeight), P, P, SZ, P], ctypes.c_int),
+                "tq4_1s_router_scored": ([P, ctypes.c_int, I64, ctypes.POINTER(_Router), P, P, P, P], ctypes.c_int),
+                "tq4_1s_int8_quantize": ([P, ctypes.c_int, ctypes.POINTER(_Int8Weight), P], ctypes.c_int),
+                "tq4_1s_int8_dequantize": ([ctypes.POINTER(_Int8Weight), P, P], ctypes.c_int),
+                "tq4_1s_linear_int8_workspace": ([I64, ctypes.POINTER(_Int8Weight)], SZ),
+                "tq4_1s_linear_int8": ([P, ctypes.c_int, I64, I64, ctypes.POINTER(_Int8Weight), P, P, SZ, P],
+                                       ctypes.c_int),
+                "tq4_1s_moe_int8_workspace": ([I64, I32, ctypes.POINTER(_Int8Weight), ctypes.POINTER(_Int8Weight)],
+                                              SZ),
+                "tq4_1s_moe_int8": ([P, ctypes.c_int, I64, P, P, I32, ctypes.POINTER(_Int8Weight),
+                                     ctypes.POINTER(_Int8Weight), P, P, SZ, P], ctypes.c_int),
             }
             for name, (args, res) in sig.items():
                 fn = getattr(lib, name)
@@ -484,4 +514,201 @@ def tq4_1s_affine_linear(x: torch.Tensor, w: AffineWeight, out: torch.Tensor | N
     ws = _workspace(lib.tq4_1s_affine_linear_workspace(m, ctypes.byref(st)), x.device, "affine")
     _check(lib.tq4_1s_affine_linear(_ptr(x), m, ctypes.byref(st), _ptr(out), _ptr(ws), ws.numel(),
                                     _stream(x.device)), "affine_linear")
+    return out
+
+
+# ------------------------------------------------------------------ scored router, int8 layers
+_DTYPES = {torch.float32: TQ_DTYPE_F32, torch.bfloat16: TQ_DTYPE_BF16, torch.float16: TQ_DTYPE_F16}
+_SCORES = {"softmax": TQ_SCORE_SOFTMAX, "sigmoid": TQ_SCORE_SIGMOID}
+_GROUP_SCORES = {"max": TQ_GROUP_MAX, "top2": TQ_GROUP_TOP2}
+
+
+def _on_device(fn):
+    """Run an entry point with its first tensor's device current (the library works on the current device)."""
+    @functools.wraps(fn)
+    def call(first, *args, **kwargs):
+        device = first.device if isinstance(first, torch.Tensor) else first.q.device
+        if device.type != "cuda" or device.index == torch.cuda.current_device():
+            return fn(first, *args, **kwargs)
+        with torch.cuda.device(device):
+            return fn(first, *args, **kwargs)
+    return call
+
+
+@functools.lru_cache(maxsize=256)
+def _router_struct(num_experts, topk, score, num_groups, topk_groups, group_score, renormalize, scale) -> _Router:
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if group_score not in _GROUP_SCORES:
+        raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}, got {group_score!r}")
+    return _Router(num_experts, topk, _SCORES[score], num_groups, topk_groups, _GROUP_SCORES[group_score],
+                   1 if renormalize else 0, scale)
+
+
+@_on_device
+def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = None, score: str = "softmax",
+                         num_groups: int = 1, topk_groups: int = 1, group_score: str = "max",
+                         renormalize: bool = True, scale: float = 1.0):
+    """(ids int32 [m][topk], weights float32 [m][topk]) from logits [m][E] (float32 or bfloat16, CUDA).
+
+    Experts are chosen by softmax or sigmoid score plus ``bias`` (float32 [E], takes part in the choice only),
+    among the ``topk_groups`` best of ``num_groups`` groups (ranked by their best expert, "max", or the sum of
+    their two best, "top2"); the weights are the scores of the chosen, renormalised if asked, times ``scale``.
+    The outputs are what tq4_1s_moe and tq4_1s_moe_int8 take."""
+    if logits.dim() != 2 or not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a CUDA float32/bfloat16 [m][E] tensor")
+    m, E = logits.shape
+    logits = logits.contiguous()
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.shape != (E,) or bias.device != logits.device:
+            raise ValueError("bias must be a float32 [E] tensor on the logits' device")
+        bias = bias.contiguous()
+    cfg = _router_struct(E, topk, score, num_groups, topk_groups, group_score, renormalize, scale)
+    ids = torch.empty((m, max(topk, 0)), dtype=torch.int32, device=logits.device)
+    w = torch.empty((m, max(topk, 0)), dtype=torch.float32, device=logits.device)
+    _check(load_library().tq4_1s_router_scored(_ptr(logits), _DTYPES[logits.dtype], m, ctypes.byref(cfg), _ptr(bias),
+                                               _ptr(ids), _ptr(w), _stream(logits.device)), "router_scored")
+    return ids, w
+
+
+@dataclass
+class Int8Weight:
+    """An int8 weight (stack): codes q int8 [E][n][k] and one float32 scale per row, wscale [E][n];
+    the weight is wscale[e][i] * q[e][i][j]."""
+    q: torch.Tensor
+    wscale: torch.Tensor
+    n: int
+    k: int
+    num_experts: int
+
+    def c_struct(self) -> _Int8Weight:
+        E, n, k = self.num_experts, self.n, self.k
+        if self.q.dtype != torch.int8 or self.q.numel() != E * n * k or not self.q.is_contiguous():
+            raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
+        if self.wscale.dtype != torch.float32 or self.wscale.numel() != E * n or not self.wscale.is_contiguous():
+            raise ValueError("Int8Weight.wscale must be a contiguous float32 tensor of num_experts * n scales")
+        if self.q.device != self.wscale.device or not self.q.is_cuda:
+            raise ValueError("Int8Weight planes must lie on one CUDA device")
+        return _Int8Weight(n, k, E, 0, self.q.data_ptr(), self.wscale.data_ptr())
+
+    @property
+    def nbytes(self) -> int:
+        return self.q.numel() + self.wscale.numel() * 4
+
+
+@_on_device
+def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
+    """Quantize W ([n][k] or [E][n][k], float32, bfloat16 or float16, CUDA, k % 32 == 0) to int8 rows."""
+    if W.dim() == 2:
+        W = W.unsqueeze(0)
+    if W.dim() != 3 or not W.is_cuda or W.dtype not in _DTYPES:
+        raise ValueError("W must be a CUDA float32/bfloat16/float16 tensor of shape [n][k] or [E][n][k]")
+    W = W.contiguous()
+    E, n, k = W.shape
+    out = Int8Weight(torch.empty((E, n, k), dtype=torch.int8, device=W.device),
+                     torch.empty((E, n), dtype=torch.float32, device=W.device), n, k, E)
+    st = out.c_struct()
+    _check(load_library().tq4_1s_int8_quantize(_ptr(W), _DTYPES[W.dtype], ctypes.byref(st), _stream(W.device)),
+           "int8_quantize")
+    return out
+
+
+@_on_device
+def tq4_1s_int8_dequantize(w: Int8Weight) -> torch.Tensor:
+    """The float32 weight [E][n][k] that w stands for."""
+    st = w.c_struct()
+    out = torch.empty((w.num_experts, w.n, w.k), dtype=torch.float32, device=w.q.device)
+    _check(load_library().tq4_1s_int8_dequantize(ctypes.byref(st), _ptr(out), _stream(out.device)), "int8_dequantize")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_int8_bytes(m: int, n: int, k: int, num_experts: int, device: int) -> int:
+    st = _Int8Weight(n, k, num_experts, 0, 0, 0)
+    return load_library().tq4_1s_linear_int8_workspace(m, ctypes.byref(st))
+
+
+def tq4_1s_linear_int8_workspace(m: int, w: Int8Weight) -> int:
+    return _linear_int8_bytes(m, w.n, w.k, w.num_experts, w.q.device.index)
+
+
+def _check_out(out, shape, dtype, device):
+    if out.shape != shape or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def _check_workspace(workspace, device):
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+@_on_device
+def tq4_1s_linear_int8(x: torch.Tensor, w: Int8Weight, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x @ W^T with int8 weights and per-token int8 activations; x [m][k] float32, bfloat16 or float16 (CUDA),
+    y of the same dtype.  Rows of x may be strided.  Without a workspace each call allocates its own (so calls on
+    different streams, and captured graphs, never share one)."""
+    if x.dim() != 2 or not x.is_cuda or x.dtype not in _DTYPES or x.shape[1] != w.k:
+        raise ValueError("x must be a CUDA float32/bfloat16/float16 [m][k] tensor with the weight's k")
+    st = w.c_struct()
+    m, device = x.shape[0], x.device
+    if w.q.device != device:
+        raise ValueError("x and the weight must lie on one device")
+    ldx = x.stride(0)
+    if x.stride(1) != 1 or ldx < w.k:
+        x = x.contiguous()
+        ldx = w.k
+    out = torch.empty((m, w.n), dtype=x.dtype, device=device) if out is None else _check_out(out, (m, w.n), x.dtype,
+                                                                                            device)
+    if workspace is None:
+        workspace = torch.empty(tq4_1s_linear_int8_workspace(m, w), dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(workspace, device)
+    _check(load_library().tq4_1s_linear_int8(x.data_ptr(), _DTYPES[x.dtype], m, ldx, ctypes.byref(st), out.data_ptr(),
+                                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                             _stream(device)), "linear_int8")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_int8_bytes(m: int, topk: int, up: tuple, down: tuple, device: int) -> int:
+    u, d = _Int8Weight(*up, 0, 0, 0), _Int8Weight(*down, 0, 0, 0)
+    return load_library().tq4_1s_moe_int8_workspace(m, topk, ctypes.byref(u), ctypes.byref(d))
+
+
+def tq4_1s_moe_int8_workspace(m: int, topk: int, up: Int8Weight, down: Int8Weight) -> int:
+    return _moe_int8_bytes(m, topk, (up.n, up.k, up.num_experts), (down.n, down.k, down.num_experts),
+                           up.q.device.index)
+
+
+@_on_device
+def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, up: Int8Weight, down: Int8Weight,
+                    out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """tq4_1s_moe with int8 experts: y_t = sum_j w_tj * down_e(bf16(relu(up_e(x_t))^2)), x [m][H] bfloat16 or float16.
+
+    ``topk_ids`` and ``topk_w`` [m][topk] come from a router (tq4_1s_router_scored, tq4_1s_router_topk)."""
+    if x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float16) or x.shape[1] != up.k:
+        raise ValueError("x must be a CUDA bfloat16/float16 [m][H] tensor with the up projection's k")
+    m, device = x.shape[0], x.device
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != m or topk_w.shape != topk_ids.shape:
+        raise ValueError("topk_ids and topk_w must both be [m][topk]")
+    if not (topk_ids.device == topk_w.device == up.q.device == down.q.device == device):
+        raise ValueError("x, the routing and the weights must lie on one device")
+    u, d = up.c_struct(), down.c_struct()
+    x = x.contiguous()
+    topk_ids = topk_ids.to(torch.int32).contiguous()
+    topk_w = topk_w.to(torch.float32).contiguous()
+    topk = topk_ids.shape[1]
+    out = torch.empty((m, up.k), dtype=x.dtype, device=device) if out is None else _check_out(out, (m, up.k), x.dtype,
+                                                                                             device)
+    if workspace is None:
+        workspace = torch.empty(tq4_1s_moe_int8_workspace(m, topk, up, down), dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(workspace, device)
+    _check(load_library().tq4_1s_moe_int8(x.data_ptr(), _DTYPES[x.dtype], m, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                          topk, ctypes.byref(u), ctypes.byref(d), out.data_ptr(),
+                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                          _stream(device)), "moe_int8")
     return out

@@ -9,6 +9,7 @@
 #include <mutex>
 #include <vector>
 
+#include "tq4_int8.h"
 #include "tq4_internal.h"
 
 #define TQ_API extern "C" __attribute__((visibility("default")))
@@ -271,6 +272,14 @@ static bool map_fp8(CUtensorMap* m, const uint8_t* q, int64_t n, int64_t k) {
     const uint32_t box[3] = {128, 128, 1};
     return make_map(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   });
+}
+
+bool encode_i8_map(CUtensorMap* m, const int8_t* base, int64_t experts, int64_t rows, int64_t k, int box_rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(k), static_cast<uint64_t>(rows), static_cast<uint64_t>(experts)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(k), static_cast<uint64_t>(rows * k)};
+  const uint32_t box[3] = {128, static_cast<uint32_t>(box_rows), 1};
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, experts > 0 ? 3 : 2, base, dims, strides, box,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -1,0 +1,530 @@
+// The int8 format (int8 codes, one fp32 scale per row): its quantizer and the
+// way back, the linear layer and the MoE on it.
+//
+// A row x quantizes to q_i = round(127 x_i / max|x|), ties to even, with scale
+// = fp32(max|x| / 127); the row it stands for is scale * q.  The rounding is
+// that of the real quotient, not of some fp32 product: half of a row's largest
+// value lies exactly on a border (63.5), so a quotient that is off by one unit
+// would round by chance there.
+#include <type_traits>
+
+#include "tq4_int8.h"
+
+#define TQ_API extern "C" __attribute__((visibility("default")))
+
+namespace tq4 {
+namespace {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) {
+  return __half2float(v);
+}
+
+// A row's divisor.  `lift` is a power of two that takes rows of tiny values
+// into the range where 127 / max|x| is finite; it changes no quotient.
+struct RowUnit {
+  float top, recip, lift, scale;
+  bool finite;
+  __device__ __forceinline__ explicit RowUnit(uint32_t top_bits) {
+    finite = top_bits < 0x7F800000u;
+    const float t = __uint_as_float(top_bits);
+    scale = finite ? __fdiv_rn(t, 127.0f) : __uint_as_float(0x7FC00000u);
+    lift = t < 1e-18f ? 0x1p64f : 1.0f;
+    top = t * lift;
+    recip = (finite && t > 0.0f) ? __fdiv_rn(127.0f, top) : 0.0f;
+  }
+  // |x| * recip is within 127 * 2^-23 (1.6e-5) of the real quotient (two
+  // roundings of relative 2^-24), so only a value that close to a border is
+  // decided again: 127 |x| against border * top, both exact in 64 bits (31 and
+  // 32 significant bits).
+  __device__ __forceinline__ int code(float x) const {
+    if (!finite) return 0;
+    const float ax = fabsf(x) * lift;
+    const float p = ax * recip;
+    float q = rintf(p);
+    const float border = floorf(p) + 0.5f;
+    if (fabsf(p - border) < 2e-5f) {
+      const double l = 127.0 * static_cast<double>(ax), r = static_cast<double>(border) * static_cast<double>(top);
+      q = l > r ? border + 0.5f : l < r ? border - 0.5f : rintf(border);
+    }
+    const int c = static_cast<int>(q);
+    return x < 0.0f ? -c : c;
+  }
+};
+
+struct RowsArgs {
+  const void* x;
+  int64_t ldx, k;
+  int8_t* q;                 // [rows][k], or sorted rows (scatter)
+  float* scale;
+  const int32_t* rows_dev;   // rows past *rows_dev are left alone (nullptr: none)
+  int32_t* counters;         // zeroed by block 0 (the split product's), or nullptr
+  int32_t ncounters;
+  // scatter: row t goes to the sorted rows of its topk slots, whose slot
+  // numbers are left in pairs; each expert's next row is cursor[expert].
+  const int32_t* ids;
+  int32_t topk, num_experts;
+  int32_t* cursor;
+  int32_t* pairs;
+};
+
+constexpr int kRowThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_constant__ RowsArgs a) {
+  __shared__ uint32_t s_top[kRowThreads / 32];
+  __shared__ int32_t s_at[64];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  if (a.counters && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.ncounters; i += kRowThreads) a.counters[i] = 0;
+  const int64_t row = blockIdx.x;
+  if (a.rows_dev && row >= __ldcg(a.rows_dev)) return;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  uint32_t top = 0;
+  for (int64_t i = threadIdx.x; i < a.k; i += kRowThreads) top = max(top, __float_as_uint(fabsf(to_f32(x[i]))));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+  if (a.ids && threadIdx.x < a.topk) {
+    const int64_t slot = row * a.topk + threadIdx.x;
+    const int32_t e = a.ids[slot];
+    int32_t at = -1;
+    if (e >= 0 && e < a.num_experts) {
+      at = atomicAdd(a.cursor + e, 1);
+      a.pairs[at] = static_cast<int32_t>(slot);
+    }
+    s_at[threadIdx.x] = at;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) top = max(top, s_top[w]);
+  const RowUnit u(top);
+  if (!u.finite && threadIdx.x == 0) raise_status(TQ_DEV_NONFINITE);
+  for (int64_t i = threadIdx.x; i < a.k; i += kRowThreads) {
+    const int8_t c = static_cast<int8_t>(u.code(to_f32(x[i])));
+    if (a.ids) {
+      for (int j = 0; j < a.topk; ++j)
+        if (s_at[j] >= 0) a.q[s_at[j] * a.k + i] = c;
+    } else {
+      a.q[row * a.k + i] = c;
+    }
+  }
+  if (a.ids) {
+    if (threadIdx.x < a.topk && s_at[threadIdx.x] >= 0) a.scale[s_at[threadIdx.x]] = u.scale;
+  } else if (threadIdx.x == 0) {
+    a.scale[row] = u.scale;
+  }
+}
+
+__global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* __restrict__ q,
+                                                              const float* __restrict__ scale,
+                                                              float* __restrict__ out, int64_t rows, int64_t k) {
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float s = scale[row];
+    for (int64_t i = threadIdx.x; i < k; i += 256) out[row * k + i] = __fmul_rn(static_cast<float>(q[row * k + i]), s);
+  }
+}
+
+// y[t] = T(sum over the slots of token t, in order, of their weighted row z).
+template <typename T>
+__global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restrict__ z, const int32_t* __restrict__ ids,
+                                                           int64_t m, int32_t topk, int64_t h, int32_t num_experts,
+                                                           T* __restrict__ y) {
+  pdl_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= m * h) return;
+  const int64_t t = i / h, n = i - t * h;
+  float s = 0.0f;
+  for (int j = 0; j < topk; ++j) {
+    const int64_t p = t * topk + j;
+    const int32_t e = ids[p];
+    if (e >= 0 && e < num_experts) s = __fadd_rn(s, __ldcg(z + p * h + n));
+  }
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (std::is_same<T, __half>::value) y[i] = __float2half_rn(s);
+    else y[i] = __float2bfloat16_rn(s);
+  }
+}
+
+// Counts each expert's slots and writes the segments (at most `chunk` rows of
+// one expert), their number, the number of rows, and each expert's first row
+// (the scatter's cursors).  One block: the slots are few bytes.
+__global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __restrict__ ids, int64_t slots,
+                                                             int32_t num_experts, int32_t chunk,
+                                                             int32_t* __restrict__ cursor, int4* __restrict__ segs,
+                                                             int32_t* __restrict__ nseg, int32_t* __restrict__ nrows) {
+  extern __shared__ int32_t count[];
+  __shared__ int32_t s_rows[32], s_segs[32];
+  __shared__ int32_t s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int e = tid; e < num_experts; e += 1024) count[e] = 0;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  for (int64_t p = tid; p < slots; p += 1024) {
+    const int32_t e = ids[p];
+    if (e >= 0 && e < num_experts) atomicAdd(&count[e], 1);
+    else s_bad = 1;
+  }
+  __syncthreads();
+  int32_t rows0 = 0, segs0 = 0;   // of the experts before this pass
+  for (int e0 = 0; e0 < num_experts; e0 += 1024) {
+    const int e = e0 + tid;
+    const int32_t c = e < num_experts ? count[e] : 0;
+    const int32_t ns = (c + chunk - 1) / chunk;
+    int32_t rows = c, nsegs = ns;   // inclusive scans: warp, then block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t r = __shfl_up_sync(0xFFFFFFFFu, rows, o), s = __shfl_up_sync(0xFFFFFFFFu, nsegs, o);
+      if (lane >= o) {
+        rows += r;
+        nsegs += s;
+      }
+    }
+    if (lane == 31) {
+      s_rows[warp] = rows;
+      s_segs[warp] = nsegs;
+    }
+    __syncthreads();
+    int32_t total_r = 0, total_s = 0, before_r = rows0, before_s = segs0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) {
+        before_r += s_rows[w];
+        before_s += s_segs[w];
+      }
+      total_r += s_rows[w];
+      total_s += s_segs[w];
+    }
+    const int32_t row = before_r + rows - c, seg = before_s + nsegs - ns;
+    if (e < num_experts) {
+      cursor[e] = row;
+      for (int32_t i = 0; i < ns; ++i) segs[seg + i] = make_int4(e, row + i * chunk, min(chunk, c - i * chunk), 0);
+    }
+    rows0 += total_r;
+    segs0 += total_s;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    *nseg = segs0;
+    *nrows = rows0;
+    if (s_bad) raise_status(TQ_DEV_BAD_ROUTING);
+  }
+}
+
+cudaError_t launch_rows(int dtype, const RowsArgs& a, int64_t rows, bool dependent, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(kRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  const cudaError_t e = dtype == TQ_DTYPE_F32    ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<float>, a)
+                        : dtype == TQ_DTYPE_BF16 ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<__nv_bfloat16>, a)
+                                                 : cudaLaunchKernelEx(&cfg, int8_rows_kernel<__half>, a);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ host
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int rc_of(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
+int elem_bytes(int dtype) { return dtype == TQ_DTYPE_F32 ? 4 : 2; }
+bool aligned_elem(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) == 0; }
+bool dtype_ok(int dtype) { return dtype == TQ_DTYPE_F32 || dtype == TQ_DTYPE_BF16 || dtype == TQ_DTYPE_F16; }
+
+int weight_ok(const tq4_1s_int8_weight* w, bool need_ptrs) {
+  if (!w || w->n <= 0 || w->k <= 0 || w->k % 32 != 0 || w->num_experts <= 0 || w->reserved != 0)
+    return TQ_ERR_INVALID_ARG;
+  if (w->n > (1ll << 30) || w->k > kInt8MaxK || w->num_experts > 4096) return TQ_ERR_INVALID_ARG;
+  if (need_ptrs) {
+    if (!w->q || !w->wscale) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(w->q) || !aligned16(w->wscale)) return TQ_ERR_ALIGNMENT;
+  }
+  return TQ_OK;
+}
+
+int sms_or_default() {
+  int sms = 148;
+  if (check_device(&sms) != TQ_OK) sms = 148;
+  return sms;
+}
+
+// How a dense product is run: tokens a tile, CTAs, and whether tiles are cut.
+struct Plan {
+  int nt, grid;
+  bool split;
+  int64_t row_tiles, tok_tiles, ksteps;
+};
+Plan plan_dense(int64_t m, int64_t n, int64_t k, int sms) {
+  Plan p;
+  p.nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 ? 128 : 256;
+  p.row_tiles = (n + 127) / 128;
+  p.tok_tiles = (m + p.nt - 1) / p.nt;
+  p.ksteps = (k + 127) / 128;
+  const int64_t tiles = p.row_tiles * p.tok_tiles;
+  p.split = p.nt <= 128 && tiles < 4 * sms;
+  const int64_t units = p.split ? tiles * p.ksteps : tiles;
+  p.grid = static_cast<int>(units < sms ? units : sms);
+  return p;
+}
+
+struct LinearLayout {
+  size_t xq, xscale, counters, partials, total;
+};
+LinearLayout linear_layout(int64_t m, int64_t k, const Plan& p) {
+  LinearLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.xq = take(static_cast<size_t>(m) * static_cast<size_t>(k));
+  L.xscale = take(static_cast<size_t>(m) * 4);
+  L.counters = take(p.split ? static_cast<size_t>(p.grid) * 4 : 0);
+  L.partials = take(p.split ? static_cast<size_t>(p.grid) * 2 * 128 * p.nt * 4 : 0);
+  L.total = off;
+  return L;
+}
+
+struct MoeLayout {
+  size_t cursor, segs, nseg, nrows, pairs, xq, xscale, h, hq, hscale, z, total;
+  int nt;
+  int64_t slots, maxseg;
+};
+MoeLayout moe_layout(int64_t m, int32_t topk, int64_t experts, int64_t H, int64_t I) {
+  MoeLayout L{};
+  L.slots = m * topk;
+  const int64_t mean = L.slots / experts;
+  L.nt = mean < 8 ? 16 : mean < 16 ? 32 : mean < 32 ? 64 : mean < 80 ? 128 : 256;
+  L.maxseg = L.slots / L.nt + (experts < L.slots ? experts : L.slots);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.cursor = take(experts * 4);
+  L.segs = take(L.maxseg * 16);
+  L.nseg = take(4);
+  L.nrows = take(4);
+  L.pairs = take(L.slots * 4);
+  L.xq = take(L.slots * H);
+  L.xscale = take(L.slots * 4);
+  L.h = take(L.slots * I * 2);
+  L.hq = take(L.slots * I);
+  L.hscale = take(L.slots * 4);
+  L.z = take(L.slots * H * 4);
+  L.total = off;
+  return L;
+}
+
+int moe_check(int64_t m, int32_t topk, const tq4_1s_int8_weight* up, const tq4_1s_int8_weight* down, bool ptrs) {
+  int rc = weight_ok(up, ptrs);
+  if (rc) return rc;
+  if ((rc = weight_ok(down, ptrs))) return rc;
+  if (m < 0 || topk <= 0 || topk > 64 || m * topk > (1ll << 26)) return TQ_ERR_INVALID_ARG;
+  if (up->num_experts != down->num_experts || up->k != down->n || up->n != down->k) return TQ_ERR_INVALID_ARG;
+  return TQ_OK;
+}
+
+}  // namespace
+}  // namespace tq4
+
+using namespace tq4;
+
+TQ_API int tq4_1s_int8_quantize(const void* W, int dtype, const tq4_1s_int8_weight* out, tq4_stream_t stream) {
+  int rc = weight_ok(out, true);
+  if (rc) return rc;
+  if (!W || !dtype_ok(dtype)) return TQ_ERR_INVALID_ARG;
+  if (!aligned16(W)) return TQ_ERR_ALIGNMENT;
+  const int64_t rows = out->n * out->num_experts;
+  if (rows > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  if ((rc = check_device(nullptr))) return rc;
+  if (take_injected_failure()) return TQ_ERR_CUDA;
+  RowsArgs a{};
+  a.x = W;
+  a.ldx = a.k = out->k;
+  a.q = out->q;
+  a.scale = out->wscale;
+  return rc_of(launch_rows(dtype, a, rows, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4_stream_t stream) {
+  int rc = weight_ok(w, true);
+  if (rc) return rc;
+  if (!W_out) return TQ_ERR_INVALID_ARG;
+  if (!aligned16(W_out)) return TQ_ERR_ALIGNMENT;
+  if ((rc = check_device(nullptr))) return rc;
+  if (take_injected_failure()) return TQ_ERR_CUDA;
+  const int64_t rows = w->n * w->num_experts;
+  int8_dequantize_kernel<<<static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20)), 256, 0,
+                           reinterpret_cast<cudaStream_t>(stream)>>>(w->q, w->wscale, W_out, rows, w->k);
+  note_launches(1);
+  return rc_of(cudaGetLastError());
+}
+
+TQ_API size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w) {
+  if (m <= 0 || m > (1ll << 24) || weight_ok(w, false) != TQ_OK || w->num_experts != 1) return 0;
+  return linear_layout(m, w->k, plan_dense(m, w->n, w->k, sms_or_default())).total;
+}
+
+TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, const tq4_1s_int8_weight* w, void* y,
+                              void* ws, size_t ws_bytes, tq4_stream_t stream) {
+  int rc = weight_ok(w, true);
+  if (rc) return rc;
+  if (w->num_experts != 1 || m < 0 || m > (1ll << 24) || !dtype_ok(dtype) || ldx < w->k || ldx > (1ll << 40))
+    return TQ_ERR_INVALID_ARG;
+  if (m == 0) return TQ_OK;
+  if (!x || !y) return TQ_ERR_INVALID_ARG;
+  if (!aligned_elem(x, dtype) || !aligned16(y)) return TQ_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  const Plan p = plan_dense(m, w->n, w->k, sms);
+  if (p.row_tiles * p.tok_tiles > INT32_MAX / p.ksteps) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  const LinearLayout L = linear_layout(m, w->k, p);
+  if (!ws || ws_bytes < L.total) return TQ_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
+  if (take_injected_failure()) return TQ_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
+  alignas(64) CUtensorMap tw, tx;
+  if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) || !encode_i8_map(&tx, xq, 0, m, w->k, p.nt))
+    return TQ_ERR_CUDA;
+  RowsArgs r{};
+  r.x = x;
+  r.ldx = ldx;
+  r.k = w->k;
+  r.q = xq;
+  r.scale = reinterpret_cast<float*>(base + L.xscale);
+  r.counters = p.split ? reinterpret_cast<int32_t*>(base + L.counters) : nullptr;
+  r.ncounters = p.grid;
+  if (launch_rows(dtype, r, m, false, st) != cudaSuccess) return TQ_ERR_CUDA;
+  Int8GemmArgs a{};
+  a.n = static_cast<int32_t>(w->n);
+  a.m = static_cast<int32_t>(m);
+  a.row_tiles = static_cast<int32_t>(p.row_tiles);
+  a.tok_tiles = static_cast<int32_t>(p.tok_tiles);
+  a.ksteps = static_cast<int32_t>(p.ksteps);
+  a.split = p.split ? 1 : 0;
+  a.mode = INT8_DENSE;
+  a.dtype = dtype;
+  a.xscale = r.scale;
+  a.wscale = w->wscale;
+  a.y = y;
+  a.partials = reinterpret_cast<int32_t*>(base + L.partials);
+  a.counters = reinterpret_cast<int32_t*>(base + L.counters);
+  return rc_of(launch_int8_gemm(tw, tx, a, p.nt, p.grid, st));
+}
+
+TQ_API size_t tq4_1s_moe_int8_workspace(int64_t m, int32_t topk, const tq4_1s_int8_weight* up,
+                                        const tq4_1s_int8_weight* down) {
+  if (moe_check(m, topk, up, down, false) != TQ_OK || m == 0) return 0;
+  return moe_layout(m, topk, up->num_experts, up->k, up->n).total;
+}
+
+TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* topk_ids, const float* topk_w,
+                           int32_t topk, const tq4_1s_int8_weight* up, const tq4_1s_int8_weight* down, void* y,
+                           void* ws, size_t ws_bytes, tq4_stream_t stream) {
+  int rc = moe_check(m, topk, up, down, true);
+  if (rc) return rc;
+  if (dtype != TQ_DTYPE_BF16 && dtype != TQ_DTYPE_F16) return TQ_ERR_INVALID_ARG;
+  if (m == 0) return TQ_OK;
+  if (!x || !y || !topk_ids || !topk_w) return TQ_ERR_INVALID_ARG;
+  if (!aligned_elem(x, dtype) || !aligned16(y) || reinterpret_cast<uintptr_t>(topk_ids) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(topk_w) % 4 != 0)
+    return TQ_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((rc = check_device(&sms))) return rc;
+  const int64_t H = up->k, I = up->n, E = up->num_experts;
+  const MoeLayout L = moe_layout(m, topk, E, H, I);
+  const int64_t rt_up = (I + 127) / 128, rt_dn = (H + 127) / 128;
+  if (L.maxseg * rt_up > INT32_MAX || L.maxseg * rt_dn > INT32_MAX) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  if (!ws || ws_bytes < L.total) return TQ_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
+  if (take_injected_failure()) return TQ_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  auto i32 = [&](size_t at) { return reinterpret_cast<int32_t*>(base + at); };
+  auto f32 = [&](size_t at) { return reinterpret_cast<float*>(base + at); };
+  int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
+  int8_t* hq = reinterpret_cast<int8_t*>(base + L.hq);
+  int4* segs = reinterpret_cast<int4*>(base + L.segs);
+  alignas(64) CUtensorMap tu, tx, td, th;
+  if (!encode_i8_map(&tu, up->q, E, I, H, 128) || !encode_i8_map(&tx, xq, 0, L.slots, H, L.nt) ||
+      !encode_i8_map(&td, down->q, E, H, I, 128) || !encode_i8_map(&th, hq, 0, L.slots, I, L.nt))
+    return TQ_ERR_CUDA;
+
+  int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(topk_ids, L.slots, static_cast<int32_t>(E), L.nt,
+                                                                    i32(L.cursor), segs, i32(L.nseg), i32(L.nrows));
+  note_launches(1);
+  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  RowsArgs r{};
+  r.x = x;
+  r.ldx = r.k = H;
+  r.q = xq;
+  r.scale = f32(L.xscale);
+  r.ids = topk_ids;
+  r.topk = topk;
+  r.num_experts = static_cast<int32_t>(E);
+  r.cursor = i32(L.cursor);
+  r.pairs = i32(L.pairs);
+  if (launch_rows(dtype, r, m, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  Int8GemmArgs a{};
+  a.n = static_cast<int32_t>(I);
+  a.row_tiles = static_cast<int32_t>(rt_up);
+  a.ksteps = static_cast<int32_t>((H + 127) / 128);
+  a.mode = INT8_UP;
+  a.segs = segs;
+  a.nseg = i32(L.nseg);
+  a.xscale = f32(L.xscale);
+  a.wscale = up->wscale;
+  a.y = base + L.h;
+  const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
+  if (launch_int8_gemm(tu, tx, a, L.nt, static_cast<int>(tiles_up < sms ? tiles_up : sms), st) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  RowsArgs g{};
+  g.x = base + L.h;
+  g.ldx = g.k = I;
+  g.q = hq;
+  g.scale = f32(L.hscale);
+  g.rows_dev = i32(L.nrows);
+  if (launch_rows(TQ_DTYPE_BF16, g, L.slots, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  a.n = static_cast<int32_t>(H);
+  a.row_tiles = static_cast<int32_t>(rt_dn);
+  a.ksteps = static_cast<int32_t>((I + 127) / 128);
+  a.mode = INT8_DOWN;
+  a.xscale = f32(L.hscale);
+  a.wscale = down->wscale;
+  a.pairs = i32(L.pairs);
+  a.topk_w = topk_w;
+  a.y = base + L.z;
+  if (launch_int8_gemm(td, th, a, L.nt, static_cast<int>(tiles_dn < sms ? tiles_dn : sms), st) != cudaSuccess)
+    return TQ_ERR_CUDA;
+  const int64_t blocks = (m * H + 255) / 256;
+  if (dtype == TQ_DTYPE_BF16)
+    int8_combine_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(f32(L.z), topk_ids, m, topk, H,
+                                                                       static_cast<int32_t>(E),
+                                                                       static_cast<__nv_bfloat16*>(y));
+  else
+    int8_combine_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(f32(L.z), topk_ids, m, topk, H,
+                                                                       static_cast<int32_t>(E),
+                                                                       static_cast<__half*>(y));
+  note_launches(1);
+  return rc_of(cudaGetLastError());
+}

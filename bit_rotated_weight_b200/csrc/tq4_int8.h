@@ -1,0 +1,37 @@
+// Shared by the int8 kernels and their entry points.
+#pragma once
+#include "tq4_internal.h"
+
+namespace tq4 {
+
+constexpr int64_t kInt8MaxK = 131072;   // 127 * 127 * k stays below 2^31
+
+enum Int8Mode : int32_t { INT8_DENSE = 0, INT8_UP = 1, INT8_DOWN = 2 };
+
+struct Int8GemmArgs {
+  int32_t n, m;             // weight rows (of one expert); dense: tokens
+  int32_t row_tiles;        // ceil(n / 128)
+  int32_t tok_tiles;        // dense: ceil(m / NT)
+  int32_t ksteps;           // ceil(k / 128)
+  int32_t split;            // cut the (tile, k step) space evenly over the CTAs
+  int32_t mode, dtype;      // Int8Mode; dense: type of y (TQ_DTYPE_*)
+  const int4* segs;         // grouped: (expert, first row, rows <= NT, -), else nullptr
+  const int32_t* nseg;      // grouped: how many
+  const float* xscale;      // [rows of xq]
+  const float* wscale;      // [experts][n]
+  const int32_t* pairs;     // down: flat slot of each sorted row
+  const float* topk_w;      // down: router weight of each slot
+  void* y;                  // dense: y [m][n]; up: h bf16 [rows][n]; down: fp32 [slots][n]
+  int32_t* partials;        // split: [grid][2][NT][128]
+  int32_t* counters;        // split: [grid], zero at launch
+};
+
+// A tensor map over int8 [experts][rows][k] (3-D), or [rows][k] where experts
+// is 0 (2-D): box 128 bytes x box_rows, 128-byte swizzle, zeros outside.
+bool encode_i8_map(CUtensorMap* m, const int8_t* base, int64_t experts, int64_t rows, int64_t k, int box_rows);
+
+// nt: 16, 32, 64, 128 or 256 tokens a tile (the box rows of tx).
+cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int nt, int grid,
+                             cudaStream_t st);
+
+}  // namespace tq4

@@ -1,0 +1,438 @@
+// The int8 tensor-core product: acc[t][n] = sum_k xq[t][k] wq[n][k] (exact
+// int32 sums), then v = (fp32(acc) sx[t]) sw[n] and one of three epilogues.
+//
+// The weight is the M operand (128 rows of W, one per tensor-memory lane) and
+// NT tokens are the N operand, so that one kernel serves a single token and a
+// long prompt: only NT changes, and any n, odd ones too, ends in plain stores.
+// Grouped launches (the experts of a MoE) walk the segments -- at most NT
+// consecutive rows of one expert -- that the routing kernel wrote.
+//   warp 0     TMA producer: 128 x 128 B of W and NT x 128 B of xq a stage;
+//   warp 1     one thread issues tcgen05.mma kind::i8 (K = 32), 4 a stage,
+//              into one of two tensor-memory accumulators;
+//   warp 2     allocates / frees tensor memory;
+//   warps 4-7  epilogue, thread = weight row.
+// With `split` the (tile, 128-byte k step) space is cut evenly over the CTAs;
+// the parts of a cut tile are left as int32 in the workspace and summed by the
+// CTA that finishes last.  Integer sums do not depend on their order, so the
+// result is the same bits whatever the cut.
+#include "tq4_int8.h"
+
+namespace tq4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;       // weight rows of a tile
+constexpr int kStep = 128;       // bytes of k per stage
+constexpr int kABytes = kRows * kStep;
+
+template <int NT>
+struct Shape {
+  static constexpr int kStageBytes = kABytes + NT * kStep;
+  static constexpr int kStages = (200 * 1024) / kStageBytes;
+  static constexpr int kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
+};
+
+template <int NT>
+struct Shared {
+  uint64_t full[Shape<NT>::kStages];
+  uint64_t empty[Shape<NT>::kStages];
+  uint64_t dfull[2];
+  uint64_t dempty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int epi_ok[2];
+  int last;
+};
+
+// kind::i8 instruction descriptor: signed 8-bit A and B, int32 D.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = global_timer();
+  while (!mbar_try_wait(addr, parity)) {
+    if (global_timer() - t0 > TQ_WAIT_NS) {
+      raise_status(TQ_DEV_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// One piece of a CTA's work: k steps [k0, k1) of a tile.
+struct Part {
+  int32_t tile, k0, k1;
+};
+
+// Walks a CTA's parts; every role walks the same ones.
+struct Walk {
+  int32_t ksteps, tiles, grid;
+  bool split;
+  int64_t at, end;   // split: units; else the next tile in `at`
+  __device__ __forceinline__ Walk(int32_t tiles_, int32_t ksteps_, bool split_)
+      : ksteps(ksteps_), tiles(tiles_), grid(static_cast<int32_t>(gridDim.x)), split(split_) {
+    if (split) {
+      at = first_unit(blockIdx.x);
+      end = first_unit(blockIdx.x + 1);
+    } else {
+      at = blockIdx.x;
+      end = tiles;
+    }
+  }
+  __device__ __forceinline__ int64_t first_unit(int32_t cta) const {
+    return static_cast<int64_t>(tiles) * ksteps * cta / grid;
+  }
+  // The CTA that holds a unit: the largest c with first_unit(c) <= unit.
+  __device__ __forceinline__ int32_t cta_of(int64_t unit) const {
+    const int64_t total = static_cast<int64_t>(tiles) * ksteps;
+    int32_t c = static_cast<int32_t>(unit * grid / total);
+    while (first_unit(c + 1) <= unit) ++c;
+    while (first_unit(c) > unit) --c;
+    return c;
+  }
+  __device__ __forceinline__ bool next(Part& p) {
+    if (at >= end) return false;
+    if (split) {
+      p.tile = static_cast<int32_t>(at / ksteps);
+      p.k0 = static_cast<int32_t>(at - static_cast<int64_t>(p.tile) * ksteps);
+      const int64_t left = end - at;
+      p.k1 = left < ksteps - p.k0 ? p.k0 + static_cast<int32_t>(left) : ksteps;
+      at += p.k1 - p.k0;
+    } else {
+      p.tile = static_cast<int32_t>(at);
+      p.k0 = 0;
+      p.k1 = ksteps;
+      at += grid;
+    }
+    return true;
+  }
+};
+
+// Where a tile lies: expert, first row of W, first token row and how many.
+struct Place {
+  int32_t expert, row0, tok0, ntok;
+};
+template <int NT>
+__device__ __forceinline__ Place place_of(const Int8GemmArgs& a, int32_t tile) {
+  Place p;
+  if (a.segs) {
+    const int32_t s = tile / a.row_tiles;
+    const int4 sg = __ldcg(a.segs + s);
+    p.expert = sg.x;
+    p.row0 = (tile - s * a.row_tiles) * kRows;
+    p.tok0 = sg.y;
+    p.ntok = sg.z;
+  } else {
+    const int32_t r = tile / a.tok_tiles;
+    p.expert = 0;
+    p.row0 = r * kRows;
+    p.tok0 = (tile - r * a.tok_tiles) * NT;
+    p.ntok = min(NT, a.m - p.tok0);
+  }
+  return p;
+}
+
+template <typename T>
+__device__ __forceinline__ void put(T* at, float v);
+template <>
+__device__ __forceinline__ void put<float>(float* at, float v) {
+  *at = v;
+}
+template <>
+__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* at, float v) {
+  *at = __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ void put<__half>(__half* at, float v) {
+  *at = __float2half_rn(v);
+}
+
+// 32 tokens (columns c0..c0+31 of the tile) of one weight row.
+template <typename T>
+__device__ __forceinline__ void store_dense(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
+                                            const int32_t (&acc)[32]) {
+  T* y = static_cast<T*>(a.y) + static_cast<int64_t>(p.tok0 + c0) * a.n + row;
+  const float* sx = a.xscale + p.tok0 + c0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (c0 + j < p.ntok) put(y + static_cast<int64_t>(j) * a.n, __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw));
+}
+
+__device__ __forceinline__ void store_up(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
+                                         const int32_t (&acc)[32]) {
+  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(p.tok0 + c0) * a.n + row;
+  const float* sx = a.xscale + p.tok0 + c0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (c0 + j < p.ntok) {
+      const float u = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw);
+      const float r = u < 0.0f ? 0.0f : u;   // (a NaN stays)
+      put(h + static_cast<int64_t>(j) * a.n, __fmul_rn(r, r));
+    }
+}
+
+__device__ __forceinline__ void store_down(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
+                                           const int32_t (&acc)[32]) {
+  const float* sx = a.xscale + p.tok0 + c0;
+  const int32_t* pairs = a.pairs + p.tok0 + c0;
+  float* z = static_cast<float*>(a.y) + row;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (c0 + j < p.ntok) {
+      const int32_t slot = __ldcg(pairs + j);
+      const float v = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw);
+      z[static_cast<int64_t>(slot) * a.n] = __fmul_rn(v, __ldcg(a.topk_w + slot));
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ Int8GemmArgs a) {
+  using S = Shape<NT>;
+  __shared__ Shared<NT> sh;
+  extern __shared__ uint8_t dyn_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.dfull[i], 1);
+      mbar_init(&sh.dempty[i], 128);
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 2) {
+    tmem_alloc(&sh.tmem_base, S::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abortp = &sh.abort_flag;
+  // A grouped launch learns its segments from the kernels before it.  A dense
+  // one knows its tiles and reads only the weight (which no kernel of this
+  // call writes) before its producer waits for the quantized activations.
+  if (a.segs) pdl_wait();
+  const int32_t tiles = a.segs ? __ldcg(a.nseg) * a.row_tiles : a.row_tiles * a.tok_tiles;
+  const bool split = a.split != 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int armed[S::kStages];
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i) armed[i] = -1;
+      int early = 0;   // stages whose weight half is already on its way
+      if (!a.segs) {
+        Walk w(tiles, a.ksteps, split);
+        Part p;
+        while (early < S::kStages && w.next(p)) {
+          const Place pl = place_of<NT>(a, p.tile);
+          for (int kk = p.k0; kk < p.k1 && early < S::kStages; ++kk, ++early) {
+            mbar_arrive_expect_tx(&sh.full[early], S::kStageBytes);
+            tma_load_3d(smem + early * S::kStageBytes, &tm_w, &sh.full[early], kk * kStep, pl.row0, pl.expert);
+          }
+        }
+        pdl_wait();
+      }
+      Walk w(tiles, a.ksteps, split);
+      Part p;
+      int li = 0;
+      bool ok = true;
+      while (ok && w.next(p)) {
+        const Place pl = place_of<NT>(a, p.tile);
+        for (int kk = p.k0; kk < p.k1; ++kk, ++li) {
+          const int s = li % S::kStages;
+          const uint32_t ph = (li / S::kStages) & 1;
+          uint8_t* st = smem + s * S::kStageBytes;
+          if (li >= early) {
+            if (!mbar_wait(&sh.empty[s], ph ^ 1u, abortp)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&sh.full[s], S::kStageBytes);
+            tma_load_3d(st, &tm_w, &sh.full[s], kk * kStep, pl.row0, pl.expert);
+          }
+          armed[s] = static_cast<int>(ph);
+          tma_load_2d(st + kABytes, &tm_x, &sh.full[s], kk * kStep, pl.tok0);
+        }
+      }
+      if (*abortp)   // let the copies in flight land before the CTA leaves
+        for (int i = 0; i < S::kStages; ++i)
+          if (armed[i] >= 0) drain_wait(&sh.full[i], static_cast<uint32_t>(armed[i]));
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_i8(kRows, NT);
+      Walk w(tiles, a.ksteps, split);
+      Part p;
+      int li = 0, ti = 0;
+      bool ok = true;
+      while (ok && w.next(p)) {
+        const int db = ti & 1;
+        if (!mbar_wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp)) break;
+        tc_fence_after();
+        const uint32_t d_addr = tmem + db * NT;
+        for (int kk = p.k0; kk < p.k1; ++kk, ++li) {
+          const int s = li % S::kStages;
+          if (!mbar_wait(&sh.full[s], (li / S::kStages) & 1, abortp)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * S::kStageBytes);
+          const uint32_t b0 = a0 + kABytes;
+#pragma unroll
+          for (int q = 0; q < kStep / 32; ++q)
+            mma_i8(d_addr, sdesc_k128(a0 + q * 32), sdesc_k128(b0 + q * 32), idesc, (kk > p.k0 || q) ? 1u : 0u);
+          mma_commit(&sh.empty[s]);
+        }
+        if (ok) mma_commit(&sh.dfull[db]);
+        ++ti;
+      }
+      mma_commit(&sh.mma_done);
+      drain_wait(&sh.mma_done, 0);
+    }
+  } else if (warp >= 4) {
+    pdl_wait();   // the scales (and the counters) come from the kernel before
+    const int t = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    Walk w(tiles, a.ksteps, split);
+    const int64_t unit0 = w.at;
+    Part p;
+    int ti = 0;
+    while (w.next(p)) {
+      const int db = ti & 1;
+      if (t == 0) sh.epi_ok[db] = mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp) ? 1 : 0;
+      named_bar_sync(1, 128);
+      if (!sh.epi_ok[db]) break;
+      tc_fence_after();
+      const Place pl = place_of<NT>(a, p.tile);
+      const int row = pl.row0 + t;
+      const uint32_t d_addr = tmem + lane_base + db * NT;
+      int32_t c_first = 0, c_last = -1;   // the CTAs that share a cut tile
+      bool finish = true;
+      if (p.k0 > 0 || p.k1 < a.ksteps) {
+        const int64_t u0 = static_cast<int64_t>(p.tile) * a.ksteps;
+        c_first = w.cta_of(u0);
+        c_last = w.cta_of(u0 + a.ksteps - 1);
+        int32_t* mine = a.partials + static_cast<int64_t>(blockIdx.x * 2 + (unit0 / a.ksteps == p.tile ? 0 : 1)) * (kRows * NT) + t;
+#pragma unroll 1
+        for (int c = 0; c < NT; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(d_addr + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < pl.ntok) __stcg(mine + (c + j) * kRows, static_cast<int32_t>(r[j]));
+        }
+        __threadfence();
+        named_bar_sync(1, 128);
+        if (t == 0) sh.last = atomicAdd(a.counters + c_first, 1) == c_last - c_first;
+        named_bar_sync(1, 128);
+        finish = sh.last != 0;
+        if (finish) __threadfence();
+      }
+      if (finish) {
+        const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < pl.ntok; c += 32) {
+          int32_t acc[32];
+          {
+            uint32_t r0[16], r1[16];
+            tmem_ld16(d_addr + c, r0);
+            if (NT > 16) tmem_ld16(d_addr + c + 16, r1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              acc[j] = static_cast<int32_t>(r0[j]);
+              acc[16 + j] = NT > 16 ? static_cast<int32_t>(r1[j]) : 0;
+            }
+          }
+          for (int32_t o = c_first; o <= c_last; ++o) {
+            if (o == static_cast<int32_t>(blockIdx.x)) continue;
+            const int32_t* theirs = a.partials + static_cast<int64_t>(o * 2 + (w.first_unit(o) / a.ksteps == p.tile ? 0 : 1)) * (kRows * NT) + t;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < NT && c + j < pl.ntok) acc[j] += __ldcg(theirs + (c + j) * kRows);
+          }
+          if (row < a.n) {
+            if (a.mode == INT8_UP) store_up(a, pl, c, row, sw, acc);
+            else if (a.mode == INT8_DOWN) store_down(a, pl, c, row, sw, acc);
+            else if (a.dtype == TQ_DTYPE_F32) store_dense<float>(a, pl, c, row, sw, acc);
+            else if (a.dtype == TQ_DTYPE_BF16) store_dense<__nv_bfloat16>(a, pl, c, row, sw, acc);
+            else store_dense<__half>(a, pl, c, row, sw, acc);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sh.dempty[db]);
+      ++ti;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, S::kTmemCols);
+}
+
+template <int NT>
+cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(int8_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Shape<NT>::kSmem));
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<NT>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, int8_gemm_kernel<NT>, tw, tx, a);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int nt, int grid,
+                             cudaStream_t st) {
+  switch (nt) {
+    case 16: return launch<16>(tw, tx, a, grid, st);
+    case 32: return launch<32>(tw, tx, a, grid, st);
+    case 64: return launch<64>(tw, tx, a, grid, st);
+    case 128: return launch<128>(tw, tx, a, grid, st);
+    default: return launch<256>(tw, tx, a, grid, st);
+  }
+}
+
+}  // namespace tq4

@@ -73,8 +73,9 @@ enum {
   TQ_DEV_SCALE_RANGE = 8   /* reserved: set by no kernel since ABI 1.02 (every finite scale is handled) */
 };
 
-/* Input dtypes of tq4_1s_quantize. */
-enum { TQ_DTYPE_F32 = 0, TQ_DTYPE_BF16 = 1 };
+/* Input dtypes of tq4_1s_quantize (F32, BF16), of tq4_1s_router_scored (F32,
+ * BF16) and of the int8 entry points (which say what they take). */
+enum { TQ_DTYPE_F32 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F16 = 2 };
 
 /* Bits of tq4_1s_weight.flags.
  *   TQ_WEIGHT_STATIC: the caller guarantees that no kernel that may still be
@@ -322,6 +323,111 @@ int tq4_1s_moe_logits(const uint16_t* x, int64_t m, const float* logits, int32_t
  * m == 0 is a no-op. */
 int tq4_1s_router_topk(const float* logits, int64_t m, int32_t num_experts, int32_t topk, int32_t* ids,
                        float* weights, tq4_stream_t stream);
+
+/* The scored router: the routing of MoE layers whose experts are chosen by
+ * softmax or sigmoid scores, with a balance bias and groups of experts (what
+ * tq4_1s_router_topk does not do).  For a token with logits z over E experts:
+ *   scores   s_i = exp(z_i) / sum exp(z) (SOFTMAX) or 1 / (1 + exp(-z_i));
+ *   choice   c_i = s_i + bias_i (c_i = s_i without a bias);
+ *   groups   the experts fall into num_groups groups of E / num_groups
+ *            consecutive ones; a group ranks by its largest c (GROUP_MAX) or
+ *            the sum of its two largest (GROUP_TOP2), and the topk_groups
+ *            best stay (equal ranks: the lower group);
+ *   ids      the topk largest c of the groups that stay, descending (equal
+ *            c: the lower id);
+ *   weights  w_j = s of the j-th (without the bias), divided by the sum over
+ *            the topk if renormalize, times scale.
+ * Scores that decide are those of fp64; without a bias the order is that of
+ * the logits.  A NaN logit counts for nothing and is never chosen, nor is an
+ * expert whose bias is NaN or +inf; either sets TQ_DEV_NONFINITE.  A logit or
+ * bias of -inf is chosen last.  Where fewer than topk experts can be chosen
+ * the last ids are -1 with weight 0 (tq4_1s_moe and tq4_1s_moe_int8 then skip
+ * the slot and set TQ_DEV_BAD_ROUTING).  A row whose scores are all 0 (every
+ * logit -inf) has weights 0. */
+enum { TQ_SCORE_SOFTMAX = 0, TQ_SCORE_SIGMOID = 1 };
+enum { TQ_GROUP_MAX = 0, TQ_GROUP_TOP2 = 1 };
+typedef struct {
+  int32_t num_experts;   /* E, 1..1024                                          */
+  int32_t topk;          /* 1..32, <= topk_groups * E / num_groups              */
+  int32_t score;         /* TQ_SCORE_*                                          */
+  int32_t num_groups;    /* 1..32, divides E; 1: no groups                      */
+  int32_t topk_groups;   /* 1..num_groups                                       */
+  int32_t group_score;   /* TQ_GROUP_*; TOP2 needs groups of 2 or more          */
+  int32_t renormalize;   /* 0 or 1                                              */
+  float scale;           /* finite factor of the weights                        */
+} tq4_1s_router;
+
+/*   logits  device [m][E], dtype F32 or BF16, aligned to its elements;
+ *   bias    device float [E], or NULL;
+ *   ids     device int32 [m][topk], written;  weights device float [m][topk],
+ *           written: what tq4_1s_moe and tq4_1s_moe_int8 take.
+ * m <= 2^32; m == 0 is a no-op. */
+int tq4_1s_router_scored(const void* logits, int dtype, int64_t m, const tq4_1s_router* cfg, const float* bias,
+                         int32_t* ids, float* weights, tq4_stream_t stream);
+
+/* An int8 weight (stack): what a checkpoint quantized to 8 bits per output
+ * channel holds, at 1 byte per weight; also the format that activations take
+ * on the way into a product, one scale per token.  A row x quantizes to
+ *   q_i = round(127 x_i / max|x|)  (ties to even, taken on the real quotient),
+ *   scale = fp32(max|x| / 127),
+ * and stands for scale * q.  A zero row has scale 0; a row that holds a NaN or
+ * an infinity has zero codes and scale NaN, and sets TQ_DEV_NONFINITE. */
+typedef struct {
+  int64_t n;            /* rows (output features), > 0                          */
+  int64_t k;            /* columns, > 0, multiple of 32, <= 131072              */
+  int32_t num_experts;  /* 1 for a dense layer, <= 4096                         */
+  int32_t reserved;     /* must be 0                                            */
+  int8_t* q;            /* device, [num_experts][n][k], 16-byte aligned         */
+  float* wscale;        /* device, [num_experts][n], 16-byte aligned            */
+} tq4_1s_int8_weight;
+
+/* Quantize W (device, [num_experts][n][k], dtype F32, BF16 or F16, 16-byte
+ * aligned) into out's planes. */
+int tq4_1s_int8_quantize(const void* W, int dtype, const tq4_1s_int8_weight* out, tq4_stream_t stream);
+
+/* Dequantize to fp32 W_out (device [num_experts][n][k], 16-byte aligned):
+ * fp32(q * scale). */
+int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4_stream_t stream);
+
+/* Bytes of workspace tq4_1s_linear_int8 needs (the quantized activations, and
+ * for few rows the parts of cut tiles); 0 on invalid arguments or m == 0. */
+size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w);
+
+/* The linear layer with int8 weights and activations: each row of x is
+ * quantized as above, then
+ *   y[t][n] = T( (sum_i xq[t][i] wq[n][i]) * xscale[t] * wscale[n] ),
+ * the sum exact in int32 on the tensor cores, the two factors applied in fp32,
+ * one rounding to T at the end; no bias.
+ *   x   device [m] rows of k elements, dtype F32, BF16 or F16, rows ldx >= k
+ *       elements apart, aligned to its elements;
+ *   y   device [m][n] of the same dtype, 16-byte aligned;
+ *   ws  device workspace of tq4_1s_linear_int8_workspace(m, w) bytes, 16-byte
+ *       aligned; it needs no initialisation, and calls that share one must not
+ *       overlap on the GPU.
+ * The output is the same bits for every m that a row is part of.  m == 0 is a
+ * no-op.  Captures into a CUDA graph. */
+int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, const tq4_1s_int8_weight* w, void* y,
+                       void* ws, size_t ws_bytes, tq4_stream_t stream);
+
+/* Bytes of workspace tq4_1s_moe_int8 needs.  0 on invalid arguments. */
+size_t tq4_1s_moe_int8_workspace(int64_t m, int32_t topk, const tq4_1s_int8_weight* up,
+                                 const tq4_1s_int8_weight* down);
+
+/* The MoE layer of tq4_1s_moe with int8 experts: for token t and slot j with
+ * expert e = topk_ids[t][j],
+ *     u = x_t W_up[e]^T,  h = bf16(relu(u)^2),  z = h W_down[e]^T,
+ *     y_t = T(sum_j topk_w[t][j] z_tj)       (slots in order, in fp32)
+ * where each product is that of tq4_1s_linear_int8 (rows of x and of h are
+ * quantized on the way in) with its result kept in fp32.
+ *   x     device [m][H], dtype BF16 or F16, aligned to its elements;
+ *   y     device [m][H] of the same dtype, 16-byte aligned;
+ *   topk_ids, topk_w, up, down, ws: as for tq4_1s_moe (the routing aligned to
+ *   its elements), with tq4_1s_moe_int8_workspace() bytes.  Ids outside [0, E) are skipped and
+ *   set TQ_DEV_BAD_ROUTING.  topk <= 64, m * topk <= 2^26.
+ * Nothing synchronizes with the host; captures into a CUDA graph. */
+int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* topk_ids, const float* topk_w, int32_t topk,
+                    const tq4_1s_int8_weight* up, const tq4_1s_int8_weight* down, void* y, void* ws,
+                    size_t ws_bytes, tq4_stream_t stream);
 
 /* The routing step of tq4_1s_moe on its own (exposed for parity tests):
  * offsets (device int32 [num_experts + 1]) = exclusive prefix of per-expert
