@@ -43,28 +43,45 @@ struct RowUnit {
     top = t * lift;
     recip = (finite && t > 0.0f) ? __fdiv_rn(127.0f, top) : 0.0f;
   }
-  // |x| * recip is within 127 * 2^-23 (1.6e-5) of the real quotient (two
-  // roundings of relative 2^-24), so only a value that close to a border is
-  // decided again: 127 |x| against border * top, both exact in 64 bits (31 and
-  // 32 significant bits).
-  __device__ __forceinline__ int code(float x) const {
-    if (!finite) return 0;
-    const float ax = fabsf(x) * lift;
-    const float p = ax * recip;
-    float q = rintf(p);
-    const float border = floorf(p) + 0.5f;
-    if (fabsf(p - border) < 2e-5f) {
-      const double l = 127.0 * static_cast<double>(ax), r = static_cast<double>(border) * static_cast<double>(top);
-      q = l > r ? border + 0.5f : l < r ? border - 0.5f : rintf(border);
-    }
-    const int c = static_cast<int>(q);
-    return x < 0.0f ? -c : c;
-  }
 };
+
+// The codes of N values, as bytes.  v * recip is within 127 * 2^-23 (1.6e-5)
+// of the real quotient (two roundings of relative 2^-24).  Adding 1.5 * 2^23
+// rounds it to a whole number, ties to even, whose low byte is the code; where
+// it lies within 2e-5 of a border, 127 v is compared with border * top, both
+// exact in 64 bits (31 and 32 significant bits).
+template <int N>
+__device__ __forceinline__ void codes_of(const RowUnit& u, const float (&v)[N], uint32_t (&bytes)[N / 4]) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t r[N];
+  float worst = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float p = __fmul_rn(v[i], u.recip);
+    const float m = __fadd_rn(p, kMagic);
+    r[i] = __float_as_uint(m);
+    worst = fmaxf(worst, fabsf(__fsub_rn(p, __fsub_rn(m, kMagic))));
+  }
+  if (worst > 0.49998f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float q = __uint_as_float(r[i]) - kMagic, d = __fmul_rn(v[i], u.recip) - q;
+      if (fabsf(d) <= 0.49998f) continue;
+      const float border = q + copysignf(0.5f, d);
+      const double l = 127.0 * static_cast<double>(v[i]), e = static_cast<double>(border) * static_cast<double>(u.top);
+      r[i] = __float_as_uint((l > e ? border + 0.5f : l < e ? border - 0.5f : rintf(border)) + kMagic);
+    }
+  }
+  if (!u.finite)   // (0 * inf and NaN end here)
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) bytes[i / 4] = prmt(prmt(r[i], r[i + 1], 0x0040), prmt(r[i + 2], r[i + 3], 0x0040), 0x5410);
+}
 
 struct RowsArgs {
   const void* x;
-  int64_t ldx, k;
+  int64_t ldx, k, rows;
   int8_t* q;                 // [rows][k], or sorted rows (scatter)
   float* scale;
   const int32_t* rows_dev;   // rows past *rows_dev are left alone (nullptr: none)
@@ -80,8 +97,149 @@ struct RowsArgs {
 
 constexpr int kRowThreads = 256;
 
+// 16 bytes of a row as fp32, and the largest |v| in them, as fp32 bits.  Bits
+// without the sign order like the values do, NaN and infinities on top, so the
+// maximum of 16-bit types is taken on pairs before any conversion.
 template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ uint32_t top(const uint4& r) {
+    return max(max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu), max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
+  }
+  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) { return t; }
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[4]) {
+    v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
+  }
+};
+struct Vec16 {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ uint32_t top(const uint4& r) {
+    const uint32_t m = 0x7FFF7FFFu;
+    const uint32_t t = __vmaxu2(__vmaxu2(r.x & m, r.y & m), __vmaxu2(r.z & m, r.w & m));
+    return max(t & 0xFFFFu, t >> 16);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> : Vec16 {
+  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) { return t << 16; }
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Vec<__half> : Vec16 {
+  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(t))));
+  }
+  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+
+// The destination rows of a scattered row (one expert slot each).
+// `threads` threads work on the row; topk (up to 64) may be more.
+__device__ __forceinline__ void take_rows(const RowsArgs& a, int64_t row, int lane, int threads, int32_t* s_at) {
+  for (int j = lane; j < a.topk; j += threads) {
+    const int64_t slot = row * a.topk + j;
+    const int32_t e = a.ids[slot];
+    int32_t at = -1;
+    if (e >= 0 && e < a.num_experts) {
+      at = atomicAdd(a.cursor + e, 1);
+      a.pairs[at] = static_cast<int32_t>(slot);
+    }
+    s_at[j] = at;
+  }
+}
+__device__ __forceinline__ void put_scale(const RowsArgs& a, int64_t row, int lane, int threads, const int32_t* s_at,
+                                          float scale) {
+  if (a.ids) {
+    for (int j = lane; j < a.topk; j += threads)
+      if (s_at[j] >= 0) a.scale[s_at[j]] = scale;
+  } else if (lane == 0) {
+    a.scale[row] = scale;
+  }
+}
+
+// TPR threads hold a row of at most TPR * NV 16-byte vectors in registers: one
+// pass over the data, all of a thread's loads in flight at once.
+template <typename T, int TPR, int NV, bool SCATTER>
 __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_constant__ RowsArgs a) {
+  using V = Vec<T>;
+  constexpr int kRowsPerBlock = kRowThreads / TPR;
+  __shared__ uint32_t s_top[kRowThreads / 32];
+  __shared__ int32_t s_at[SCATTER ? kRowsPerBlock : 1][64];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  if (a.counters && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.ncounters; i += kRowThreads) a.counters[i] = 0;
+  const int64_t rows = a.rows_dev ? __ldcg(a.rows_dev) : a.rows;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + sub;
+  const bool live = row < rows;
+  if (TPR == 32 ? !live : static_cast<int64_t>(blockIdx.x) * kRowsPerBlock >= rows) return;
+  const int nvec = static_cast<int>(a.k) / V::N;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx);
+  uint4 raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) raw[i] = live && lane + i * TPR < nvec ? __ldcs(x + lane + i * TPR) : make_uint4(0, 0, 0, 0);
+  if (SCATTER && live) take_rows(a, row, lane, TPR, s_at[sub]);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) top = max(top, V::top(raw[i]));
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  if (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TPR / 32; ++w) top = max(top, s_top[sub * (TPR / 32) + w]);
+  } else {
+    __syncwarp();
+  }
+  if (!live) return;
+  const RowUnit u(V::top_f32(top));
+  if (!u.finite && lane == 0) raise_status(TQ_DEV_NONFINITE);
+  put_scale(a, row, lane, TPR, s_at[SCATTER ? sub : 0], u.scale);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = lane + i * TPR;
+    if (at >= nvec) break;
+    float v[V::N];
+    V::unpack(raw[i], v);
+    if (u.lift != 1.0f)
+#pragma unroll
+      for (int j = 0; j < V::N; ++j) v[j] *= u.lift;
+    uint32_t c[V::N / 4];
+    codes_of(u, v, c);
+    auto put = [&](int64_t to) {
+      uint32_t* q = reinterpret_cast<uint32_t*>(a.q + to * a.k) + static_cast<int64_t>(at) * (V::N / 4);
+      if constexpr (V::N == 8) *reinterpret_cast<uint2*>(q) = make_uint2(c[0], c[1]);
+      else *q = c[0];
+    };
+    if constexpr (SCATTER) {
+      for (int j = 0; j < a.topk; ++j)
+        if (s_at[sub][j] >= 0) put(s_at[sub][j]);
+    } else {
+      put(row);
+    }
+  }
+}
+
+// Rows of any length and alignment, read twice.
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) int8_rows_any_kernel(const __grid_constant__ RowsArgs a) {
   __shared__ uint32_t s_top[kRowThreads / 32];
   __shared__ int32_t s_at[64];
   pdl_wait();
@@ -92,68 +250,103 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_con
   if (a.rows_dev && row >= __ldcg(a.rows_dev)) return;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   uint32_t top = 0;
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < a.k; i += kRowThreads) top = max(top, __float_as_uint(fabsf(to_f32(x[i]))));
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-  if (a.ids && threadIdx.x < a.topk) {
-    const int64_t slot = row * a.topk + threadIdx.x;
-    const int32_t e = a.ids[slot];
-    int32_t at = -1;
-    if (e >= 0 && e < a.num_experts) {
-      at = atomicAdd(a.cursor + e, 1);
-      a.pairs[at] = static_cast<int32_t>(slot);
-    }
-    s_at[threadIdx.x] = at;
-  }
+  if (a.ids) take_rows(a, row, threadIdx.x, kRowThreads, s_at);
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kRowThreads / 32; ++w) top = max(top, s_top[w]);
   const RowUnit u(top);
   if (!u.finite && threadIdx.x == 0) raise_status(TQ_DEV_NONFINITE);
-  for (int64_t i = threadIdx.x; i < a.k; i += kRowThreads) {
-    const int8_t c = static_cast<int8_t>(u.code(to_f32(x[i])));
+  put_scale(a, row, threadIdx.x, kRowThreads, s_at, u.scale);
+#pragma unroll 2
+  for (int64_t i = 4 * threadIdx.x; i < a.k; i += 4 * kRowThreads) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = to_f32(x[i + j]) * u.lift;
+    uint32_t c[1];
+    codes_of(u, v, c);
     if (a.ids) {
       for (int j = 0; j < a.topk; ++j)
-        if (s_at[j] >= 0) a.q[s_at[j] * a.k + i] = c;
+        if (s_at[j] >= 0) *reinterpret_cast<uint32_t*>(a.q + s_at[j] * a.k + i) = c[0];
     } else {
-      a.q[row * a.k + i] = c;
+      *reinterpret_cast<uint32_t*>(a.q + row * a.k + i) = c[0];
     }
-  }
-  if (a.ids) {
-    if (threadIdx.x < a.topk && s_at[threadIdx.x] >= 0) a.scale[s_at[threadIdx.x]] = u.scale;
-  } else if (threadIdx.x == 0) {
-    a.scale[row] = u.scale;
   }
 }
 
+constexpr int kDeqGroups = 4;   // groups of 4 codes per thread
+
 __global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* __restrict__ q,
                                                               const float* __restrict__ scale,
-                                                              float* __restrict__ out, int64_t rows, int64_t k) {
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const float s = scale[row];
-    for (int64_t i = threadIdx.x; i < k; i += 256) out[row * k + i] = __fmul_rn(static_cast<float>(q[row * k + i]), s);
+                                                              float* __restrict__ out, int64_t rows, int32_t kg) {
+  // kg: groups of 4 codes in a row.  The block's first group is located with
+  // one 64-bit division, the others from there.
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kDeqGroups);
+  const int64_t row0 = first / kg, total = rows * kg;
+  const uint32_t col0 = static_cast<uint32_t>(first - row0 * kg);
+  char4 c[kDeqGroups];
+  float s[kDeqGroups];
+#pragma unroll
+  for (int j = 0; j < kDeqGroups; ++j) {
+    const uint32_t at = threadIdx.x + 256 * j;
+    if (first + at >= total) break;
+    c[j] = __ldcs(reinterpret_cast<const char4*>(q) + first + at);
+    s[j] = __ldg(scale + row0 + (col0 + at) / static_cast<uint32_t>(kg));
+  }
+#pragma unroll
+  for (int j = 0; j < kDeqGroups; ++j) {
+    const uint32_t at = threadIdx.x + 256 * j;
+    if (first + at >= total) break;
+    __stcs(reinterpret_cast<float4*>(out) + first + at,
+           make_float4(__fmul_rn(static_cast<float>(c[j].x), s[j]), __fmul_rn(static_cast<float>(c[j].y), s[j]),
+                       __fmul_rn(static_cast<float>(c[j].z), s[j]), __fmul_rn(static_cast<float>(c[j].w), s[j])));
   }
 }
 
 // y[t] = T(sum over the slots of token t, in order, of their weighted row z).
+// Four outputs a thread; the rows of up to eight slots are requested before
+// the first is added.
 template <typename T>
 __global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restrict__ z, const int32_t* __restrict__ ids,
-                                                           int64_t m, int32_t topk, int64_t h, int32_t num_experts,
+                                                           int64_t m, int32_t topk, int32_t hg, int32_t num_experts,
                                                            T* __restrict__ y) {
   pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= m * h) return;
-  const int64_t t = i / h, n = i - t * h;
-  float s = 0.0f;
-  for (int j = 0; j < topk; ++j) {
-    const int64_t p = t * topk + j;
-    const int32_t e = ids[p];
-    if (e >= 0 && e < num_experts) s = __fadd_rn(s, __ldcg(z + p * h + n));
+  if (i >= m * hg) return;
+  const int64_t t = i / hg;
+  const int32_t n = static_cast<int32_t>(i - t * hg);
+  const float4* zt = reinterpret_cast<const float4*>(z) + t * topk * hg + n;
+  const int32_t* idt = ids + t * topk;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j0 = 0; j0 < topk; j0 += 8) {
+    float4 v[8];
+    bool ok[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int32_t e = j0 + j < topk ? __ldg(idt + j0 + j) : -1;
+      ok[j] = e >= 0 && e < num_experts;
+      if (ok[j]) v[j] = __ldcs(zt + static_cast<int64_t>(j0 + j) * hg);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (ok[j]) {
+        s.x = __fadd_rn(s.x, v[j].x);
+        s.y = __fadd_rn(s.y, v[j].y);
+        s.z = __fadd_rn(s.z, v[j].z);
+        s.w = __fadd_rn(s.w, v[j].w);
+      }
   }
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (std::is_same<T, __half>::value) y[i] = __float2half_rn(s);
-    else y[i] = __float2bfloat16_rn(s);
+  uint2 o;
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 lo = __floats2half2_rn(s.x, s.y), hi = __floats2half2_rn(s.z, s.w);
+    o = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    o = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
+  *(reinterpret_cast<uint2*>(y) + i) = o;
 }
 
 // Counts each expert's slots and writes the segments (at most `chunk` rows of
@@ -220,9 +413,29 @@ __global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __re
   }
 }
 
-cudaError_t launch_rows(int dtype, const RowsArgs& a, int64_t rows, bool dependent, cudaStream_t st) {
+template <typename T, int TPR, int NV>
+cudaError_t launch_rows_as(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kRowThreads / TPR - 1) / (kRowThreads / TPR)));
+  return a.ids ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, true>, a)
+               : cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, false>, a);
+}
+
+template <typename T>
+cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
+  const int64_t nvec = a.k / Vec<T>::N;
+  const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % Vec<T>::N == 0;
+  if (wide && nvec <= 32 * 4) return launch_rows_as<T, 32, 4>(a, cfg);
+  if (wide && nvec <= 128 * 4) return launch_rows_as<T, 128, 4>(a, cfg);
+  if (wide && nvec <= 256 * 4) return launch_rows_as<T, 256, 4>(a, cfg);
+  if (wide && nvec <= 256 * 8) return launch_rows_as<T, 256, 8>(a, cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
+  return cudaLaunchKernelEx(&cfg, int8_rows_any_kernel<T>, a);
+}
+
+// `dependent`: may be set up while the kernel before it still runs (it waits
+// for its end before its first load).
+cudaError_t launch_rows(int dtype, const RowsArgs& a, bool dependent, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
   cfg.blockDim = dim3(kRowThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -230,9 +443,9 @@ cudaError_t launch_rows(int dtype, const RowsArgs& a, int64_t rows, bool depende
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 1 : 0;
-  const cudaError_t e = dtype == TQ_DTYPE_F32    ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<float>, a)
-                        : dtype == TQ_DTYPE_BF16 ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<__nv_bfloat16>, a)
-                                                 : cudaLaunchKernelEx(&cfg, int8_rows_kernel<__half>, a);
+  const cudaError_t e = dtype == TQ_DTYPE_F32    ? launch_rows_of<float>(a, cfg)
+                        : dtype == TQ_DTYPE_BF16 ? launch_rows_of<__nv_bfloat16>(a, cfg)
+                                                 : launch_rows_of<__half>(a, cfg);
   if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
@@ -359,9 +572,10 @@ TQ_API int tq4_1s_int8_quantize(const void* W, int dtype, const tq4_1s_int8_weig
   RowsArgs a{};
   a.x = W;
   a.ldx = a.k = out->k;
+  a.rows = rows;
   a.q = out->q;
   a.scale = out->wscale;
-  return rc_of(launch_rows(dtype, a, rows, false, reinterpret_cast<cudaStream_t>(stream)));
+  return rc_of(launch_rows(dtype, a, false, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4_stream_t stream) {
@@ -371,9 +585,11 @@ TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4
   if (!aligned16(W_out)) return TQ_ERR_ALIGNMENT;
   if ((rc = check_device(nullptr))) return rc;
   if (take_injected_failure()) return TQ_ERR_CUDA;
-  const int64_t rows = w->n * w->num_experts;
-  int8_dequantize_kernel<<<static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20)), 256, 0,
-                           reinterpret_cast<cudaStream_t>(stream)>>>(w->q, w->wscale, W_out, rows, w->k);
+  const int64_t rows = w->n * w->num_experts, kg = w->k / 4;
+  const int64_t blocks = (rows * kg + 256 * kDeqGroups - 1) / (256 * kDeqGroups);
+  if (blocks > INT32_MAX) return TQ_ERR_INVALID_ARG;
+  int8_dequantize_kernel<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      w->q, w->wscale, W_out, rows, static_cast<int32_t>(kg));
   note_launches(1);
   return rc_of(cudaGetLastError());
 }
@@ -410,11 +626,12 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   r.x = x;
   r.ldx = ldx;
   r.k = w->k;
+  r.rows = m;
   r.q = xq;
   r.scale = reinterpret_cast<float*>(base + L.xscale);
   r.counters = p.split ? reinterpret_cast<int32_t*>(base + L.counters) : nullptr;
   r.ncounters = p.grid;
-  if (launch_rows(dtype, r, m, false, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(dtype, r, false, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(w->n);
   a.m = static_cast<int32_t>(m);
@@ -477,6 +694,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   RowsArgs r{};
   r.x = x;
   r.ldx = r.k = H;
+  r.rows = m;
   r.q = xq;
   r.scale = f32(L.xscale);
   r.ids = topk_ids;
@@ -484,7 +702,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   r.num_experts = static_cast<int32_t>(E);
   r.cursor = i32(L.cursor);
   r.pairs = i32(L.pairs);
-  if (launch_rows(dtype, r, m, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(dtype, r, true, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(I);
   a.row_tiles = static_cast<int32_t>(rt_up);
@@ -501,10 +719,11 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   RowsArgs g{};
   g.x = base + L.h;
   g.ldx = g.k = I;
+  g.rows = L.slots;
   g.q = hq;
   g.scale = f32(L.hscale);
   g.rows_dev = i32(L.nrows);
-  if (launch_rows(TQ_DTYPE_BF16, g, L.slots, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(TQ_DTYPE_BF16, g, true, st) != cudaSuccess) return TQ_ERR_CUDA;
   a.n = static_cast<int32_t>(H);
   a.row_tiles = static_cast<int32_t>(rt_dn);
   a.ksteps = static_cast<int32_t>((I + 127) / 128);
@@ -516,15 +735,12 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   a.y = base + L.z;
   if (launch_int8_gemm(td, th, a, L.nt, static_cast<int>(tiles_dn < sms ? tiles_dn : sms), st) != cudaSuccess)
     return TQ_ERR_CUDA;
-  const int64_t blocks = (m * H + 255) / 256;
+  const int32_t hg = static_cast<int32_t>(H / 4), experts = static_cast<int32_t>(E);
+  const unsigned blocks = static_cast<unsigned>((m * hg + 255) / 256);
   if (dtype == TQ_DTYPE_BF16)
-    int8_combine_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(f32(L.z), topk_ids, m, topk, H,
-                                                                       static_cast<int32_t>(E),
-                                                                       static_cast<__nv_bfloat16*>(y));
+    int8_combine_kernel<<<blocks, 256, 0, st>>>(f32(L.z), topk_ids, m, topk, hg, experts, static_cast<__nv_bfloat16*>(y));
   else
-    int8_combine_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(f32(L.z), topk_ids, m, topk, H,
-                                                                       static_cast<int32_t>(E),
-                                                                       static_cast<__half*>(y));
+    int8_combine_kernel<<<blocks, 256, 0, st>>>(f32(L.z), topk_ids, m, topk, hg, experts, static_cast<__half*>(y));
   note_launches(1);
   return rc_of(cudaGetLastError());
 }

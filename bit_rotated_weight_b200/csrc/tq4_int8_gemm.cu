@@ -44,6 +44,9 @@ struct Shared {
   int abort_flag;
   int epi_ok[2];
   int last;
+  alignas(16) float sx[2][NT < 32 ? 32 : NT];       // the tile's token scales,
+  alignas(16) float tw[2][NT];       // router weights and
+  alignas(16) int32_t slot[2][NT];   // slots (down only)
 };
 
 // kind::i8 instruction descriptor: signed 8-bit A and B, int32 D.
@@ -76,42 +79,39 @@ struct Part {
   int32_t tile, k0, k1;
 };
 
-// Walks a CTA's parts; every role walks the same ones.
+// Walks a CTA's parts; every role walks the same ones.  Cut evenly, CTA c
+// holds the units [c q + min(c, r), (c+1) q + min(c+1, r)).
 struct Walk {
-  int32_t ksteps, tiles, grid;
+  int32_t ksteps, grid, per, rest;
   bool split;
-  int64_t at, end;   // split: units; else the next tile in `at`
-  __device__ __forceinline__ Walk(int32_t tiles_, int32_t ksteps_, bool split_)
-      : ksteps(ksteps_), tiles(tiles_), grid(static_cast<int32_t>(gridDim.x)), split(split_) {
+  int32_t at, end;   // split: units; else tiles
+  __device__ __forceinline__ Walk(int32_t tiles, int32_t ksteps_, bool split_)
+      : ksteps(ksteps_), grid(static_cast<int32_t>(gridDim.x)), split(split_) {
     if (split) {
+      per = tiles * ksteps / grid;
+      rest = tiles * ksteps - per * grid;
       at = first_unit(blockIdx.x);
       end = first_unit(blockIdx.x + 1);
     } else {
+      per = rest = 0;
       at = blockIdx.x;
       end = tiles;
     }
   }
-  __device__ __forceinline__ int64_t first_unit(int32_t cta) const {
-    return static_cast<int64_t>(tiles) * ksteps * cta / grid;
-  }
-  // The CTA that holds a unit: the largest c with first_unit(c) <= unit.
-  __device__ __forceinline__ int32_t cta_of(int64_t unit) const {
-    const int64_t total = static_cast<int64_t>(tiles) * ksteps;
-    int32_t c = static_cast<int32_t>(unit * grid / total);
-    while (first_unit(c + 1) <= unit) ++c;
-    while (first_unit(c) > unit) --c;
-    return c;
+  __device__ __forceinline__ int32_t first_unit(int32_t cta) const { return cta * per + min(cta, rest); }
+  __device__ __forceinline__ int32_t cta_of(int32_t unit) const {
+    const int32_t big = rest * (per + 1);
+    return unit < big ? unit / (per + 1) : rest + (unit - big) / per;
   }
   __device__ __forceinline__ bool next(Part& p) {
     if (at >= end) return false;
     if (split) {
-      p.tile = static_cast<int32_t>(at / ksteps);
-      p.k0 = static_cast<int32_t>(at - static_cast<int64_t>(p.tile) * ksteps);
-      const int64_t left = end - at;
-      p.k1 = left < ksteps - p.k0 ? p.k0 + static_cast<int32_t>(left) : ksteps;
+      p.tile = at / ksteps;
+      p.k0 = at - p.tile * ksteps;
+      p.k1 = min(ksteps, p.k0 + end - at);
       at += p.k1 - p.k0;
     } else {
-      p.tile = static_cast<int32_t>(at);
+      p.tile = at;
       p.k0 = 0;
       p.k1 = ksteps;
       at += grid;
@@ -144,57 +144,47 @@ __device__ __forceinline__ Place place_of(const Int8GemmArgs& a, int32_t tile) {
   return p;
 }
 
-template <typename T>
-__device__ __forceinline__ void put(T* at, float v);
-template <>
-__device__ __forceinline__ void put<float>(float* at, float v) {
-  *at = v;
-}
-template <>
-__device__ __forceinline__ void put<__nv_bfloat16>(__nv_bfloat16* at, float v) {
-  *at = __float2bfloat16_rn(v);
-}
-template <>
-__device__ __forceinline__ void put<__half>(__half* at, float v) {
-  *at = __float2half_rn(v);
+// The 32 tokens (columns c0.. of the tile) of one weight row, from their sums.
+// Scales come from shared memory: a global load between the stores would wait
+// for its latency 32 times over (the compiler cannot move it past a store).
+__device__ __forceinline__ void scale32(const float* sx, float sw, const int32_t (&acc)[32], float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const float4 s = *reinterpret_cast<const float4*>(sx + j);
+    v[j] = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), s.x), sw);
+    v[j + 1] = __fmul_rn(__fmul_rn(static_cast<float>(acc[j + 1]), s.y), sw);
+    v[j + 2] = __fmul_rn(__fmul_rn(static_cast<float>(acc[j + 2]), s.z), sw);
+    v[j + 3] = __fmul_rn(__fmul_rn(static_cast<float>(acc[j + 3]), s.w), sw);
+  }
 }
 
-// 32 tokens (columns c0..c0+31 of the tile) of one weight row.
-template <typename T>
-__device__ __forceinline__ void store_dense(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
-                                            const int32_t (&acc)[32]) {
-  T* y = static_cast<T*>(a.y) + static_cast<int64_t>(p.tok0 + c0) * a.n + row;
-  const float* sx = a.xscale + p.tok0 + c0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (c0 + j < p.ntok) put(y + static_cast<int64_t>(j) * a.n, __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw));
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if (BF16) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void store_up(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
-                                         const int32_t (&acc)[32]) {
-  __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(p.tok0 + c0) * a.n + row;
-  const float* sx = a.xscale + p.tok0 + c0;
+// 16-bit rows y[token][n] from 32 tokens of one weight row per lane.  Where n
+// is even, lanes pair up: of two tokens the even lane takes the first and the
+// odd lane the second, for both rows, so that each store is 4 bytes.
+template <bool BF16>
+__device__ __forceinline__ void store16(uint16_t* y, int64_t n, int row, int rows_left, bool pairs, int ntok,
+                                        const float (&v)[32]) {
+  if (pairs) {
+    const bool odd = row & 1;
+    uint32_t* at = reinterpret_cast<uint32_t*>(y + (odd ? n : 0) + (row & ~1));
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (c0 + j < p.ntok) {
-      const float u = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw);
-      const float r = u < 0.0f ? 0.0f : u;   // (a NaN stays)
-      put(h + static_cast<int64_t>(j) * a.n, __fmul_rn(r, r));
+    for (int j = 0; j < 32; j += 2) {
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+      const uint32_t w = odd ? pack16<BF16>(other, v[j + 1]) : pack16<BF16>(v[j], other);
+      if (rows_left > 0 && j + (odd ? 1 : 0) < ntok) at[j * (n >> 1)] = w;
     }
-}
-
-__device__ __forceinline__ void store_down(const Int8GemmArgs& a, const Place& p, int c0, int row, float sw,
-                                           const int32_t (&acc)[32]) {
-  const float* sx = a.xscale + p.tok0 + c0;
-  const int32_t* pairs = a.pairs + p.tok0 + c0;
-  float* z = static_cast<float*>(a.y) + row;
+  } else if (rows_left > 0) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (c0 + j < p.ntok) {
-      const int32_t slot = __ldcg(pairs + j);
-      const float v = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), __ldcg(sx + j)), sw);
-      z[static_cast<int64_t>(slot) * a.n] = __fmul_rn(v, __ldcg(a.topk_w + slot));
-    }
+    for (int j = 0; j < 32; ++j)
+      if (j < ntok) y[j * n + row] = static_cast<uint16_t>(pack16<BF16>(v[j], 0.0f));
+  }
 }
 
 template <int NT>
@@ -319,25 +309,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Walk w(tiles, a.ksteps, split);
-    const int64_t unit0 = w.at;
+    const int32_t tile0 = split ? w.at / a.ksteps : 0;
     Part p;
     int ti = 0;
     while (w.next(p)) {
       const int db = ti & 1;
+      const Place pl = place_of<NT>(a, p.tile);
+      // (the buffers of the last tile but one: every thread has left it)
+      for (int j = t; j < NT; j += 128) {
+        const bool in = j < pl.ntok;
+        sh.sx[db][j] = in ? __ldcg(a.xscale + pl.tok0 + j) : 0.0f;
+        if (a.mode == INT8_DOWN) {
+          const int32_t slot = in ? __ldcg(a.pairs + pl.tok0 + j) : 0;
+          sh.slot[db][j] = slot;
+          sh.tw[db][j] = in ? __ldg(a.topk_w + slot) : 0.0f;
+        }
+      }
       if (t == 0) sh.epi_ok[db] = mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp) ? 1 : 0;
       named_bar_sync(1, 128);
       if (!sh.epi_ok[db]) break;
       tc_fence_after();
-      const Place pl = place_of<NT>(a, p.tile);
       const int row = pl.row0 + t;
       const uint32_t d_addr = tmem + lane_base + db * NT;
       int32_t c_first = 0, c_last = -1;   // the CTAs that share a cut tile
       bool finish = true;
       if (p.k0 > 0 || p.k1 < a.ksteps) {
-        const int64_t u0 = static_cast<int64_t>(p.tile) * a.ksteps;
+        const int32_t u0 = p.tile * a.ksteps;
         c_first = w.cta_of(u0);
         c_last = w.cta_of(u0 + a.ksteps - 1);
-        int32_t* mine = a.partials + static_cast<int64_t>(blockIdx.x * 2 + (unit0 / a.ksteps == p.tile ? 0 : 1)) * (kRows * NT) + t;
+        int32_t* mine = a.partials + static_cast<int64_t>(blockIdx.x * 2 + (tile0 == p.tile ? 0 : 1)) * (kRows * NT) + t;
 #pragma unroll 1
         for (int c = 0; c < NT; c += 16) {
           uint32_t r[16];
@@ -377,12 +377,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j)
               if (j < NT && c + j < pl.ntok) acc[j] += __ldcg(theirs + (c + j) * kRows);
           }
-          if (row < a.n) {
-            if (a.mode == INT8_UP) store_up(a, pl, c, row, sw, acc);
-            else if (a.mode == INT8_DOWN) store_down(a, pl, c, row, sw, acc);
-            else if (a.dtype == TQ_DTYPE_F32) store_dense<float>(a, pl, c, row, sw, acc);
-            else if (a.dtype == TQ_DTYPE_BF16) store_dense<__nv_bfloat16>(a, pl, c, row, sw, acc);
-            else store_dense<__half>(a, pl, c, row, sw, acc);
+          float v[32];
+          scale32(sh.sx[db] + c, sw, acc, v);
+          const int left = pl.ntok - c;
+          const int64_t tok = pl.tok0 + c;
+          if (a.mode == INT8_DOWN) {
+            float* z = static_cast<float*>(a.y) + row;
+            if (row < a.n)
+#pragma unroll
+              for (int j = 0; j < (NT < 32 ? NT : 32); ++j)
+                if (j < left) z[static_cast<int64_t>(sh.slot[db][c + j]) * a.n] = __fmul_rn(v[j], sh.tw[db][c + j]);
+          } else if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F32) {
+            float* y = static_cast<float*>(a.y) + tok * a.n + row;
+            if (row < a.n)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < left) y[static_cast<int64_t>(j) * a.n] = v[j];
+          } else {
+            if (a.mode == INT8_UP) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float r = v[j] < 0.0f ? 0.0f : v[j];   // (a NaN stays)
+                v[j] = __fmul_rn(r, r);
+              }
+            }
+            uint16_t* y = static_cast<uint16_t*>(a.y) + tok * a.n;
+            const bool pairs = (a.n & 1) == 0;
+            if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F16) store16<false>(y, a.n, row, a.n - row, pairs, left, v);
+            else store16<true>(y, a.n, row, a.n - row, pairs, left, v);
           }
         }
       }
