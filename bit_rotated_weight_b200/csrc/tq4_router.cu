@@ -90,6 +90,7 @@ __device__ __noinline__ void slow_row(const RouterArgs& a, int64_t t, double* ch
   auto score = [&](int e) { return a.sigmoid ? part(e) : sum > 0.0 ? part(e) / sum : 0.0; };
   const bool grouped = a.keep < a.groups;
   const bool by_score = grouped && a.top2 && !a.bias;   // sums need the scores themselves
+#pragma unroll 4
   for (int i = 0; i < per; ++i) {
     const int e = lane + 32 * i;
     if (e >= a.experts) break;
@@ -113,20 +114,30 @@ __device__ __noinline__ void slow_row(const RouterArgs& a, int64_t t, double* ch
   if (grouped) {
     __syncwarp();
     const int size = a.experts / a.groups;
-    double first = -kInf, second = -kInf;   // lane g ranks group g
-    if (lane < a.groups)
-      for (int i = 0; i < size; ++i) {
-        const double c = choice[lane * size + i];
+    int shift = 0;   // 2^shift lanes rank a group
+    while ((a.groups << (shift + 1)) <= 32) ++shift;
+    const int g = lane >> shift, step = 1 << shift;
+    double first = -kInf, second = -kInf;
+    if (g < a.groups)
+      for (int i = lane & (step - 1); i < size; i += step) {
+        const double c = choice[g * size + i];
         second = fmax(second, fmin(first, c));
         first = fmax(first, c);
       }
+    for (int o = step >> 1; o > 0; o >>= 1) {
+      const double f = __shfl_xor_sync(0xFFFFFFFFu, first, o), s = __shfl_xor_sync(0xFFFFFFFFu, second, o);
+      second = fmax(fmin(first, f), fmax(second, s));
+      first = fmax(first, f);
+    }
     const double rank = a.top2 ? first + second : first;
     int better = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double other = __shfl_sync(0xFFFFFFFFu, rank, g);
-      better += (other > rank || (other == rank && g < lane)) ? 1 : 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const double other = __shfl_sync(0xFFFFFFFFu, rank, o << shift);
+      better += (other > rank || (other == rank && o < g)) ? 1 : 0;
     }
-    const uint32_t kept = __ballot_sync(0xFFFFFFFFu, lane < a.groups && better < a.keep);
+    uint32_t kept = 0;
+    const uint32_t kept_lanes = __ballot_sync(0xFFFFFFFFu, g < a.groups && better < a.keep);
+    for (int o = 0; o < a.groups; ++o) kept |= ((kept_lanes >> (o << shift)) & 1u) << o;
     __syncwarp();
     for (int i = 0; i < per; ++i) {
       const int e = lane + 32 * i;
@@ -136,26 +147,36 @@ __device__ __noinline__ void slow_row(const RouterArgs& a, int64_t t, double* ch
     }
   }
   int my_id = -1;   // lane j: the j-th choice
-  for (int j = 0; j < a.topk; ++j) {
-    double bc = -kInf;
-    int be = INT32_MAX;
+  double bc = -kInf;   // the lane's best
+  int be = INT32_MAX;
+  auto best_of_lane = [&]() {
+    bc = -kInf;
+    be = INT32_MAX;
+#pragma unroll 4
     for (int i = 0; i < per; ++i)
       if (((open >> i) & 1u) && (be == INT32_MAX || choice[lane + 32 * i] > bc)) {
         be = lane + 32 * i;
         bc = choice[be];
       }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const double oc = __shfl_xor_sync(0xFFFFFFFFu, bc, o);
-      const int oe = __shfl_xor_sync(0xFFFFFFFFu, be, o);
-      if (oe != INT32_MAX && (be == INT32_MAX || oc > bc || (oc == bc && oe < be))) {
-        bc = oc;
-        be = oe;
-      }
+  };
+  best_of_lane();
+  for (int j = 0; j < a.topk; ++j) {
+    // fp64 values as 64-bit integers of the same order (-0 as 0), the halves
+    // reduced one after the other, then the lowest id
+    const int64_t bits = __double_as_longlong(bc + 0.0);
+    const int64_t key = bits ^ ((bits >> 63) & INT64_MAX);
+    const bool has = be != INT32_MAX;
+    if (!__any_sync(0xFFFFFFFFu, has)) break;
+    const int32_t hi = static_cast<int32_t>(key >> 32);
+    const int32_t top_hi = __reduce_max_sync(0xFFFFFFFFu, has ? hi : INT32_MIN);
+    const bool in = has && hi == top_hi;
+    const uint32_t top_lo = __reduce_max_sync(0xFFFFFFFFu, in ? static_cast<uint32_t>(key) : 0u);
+    const int id = __reduce_min_sync(0xFFFFFFFFu, in && static_cast<uint32_t>(key) == top_lo ? be : INT32_MAX);
+    if (lane == j) my_id = id;
+    if ((id & 31) == lane) {
+      open &= ~(1u << (id >> 5));
+      best_of_lane();
     }
-    if (be == INT32_MAX) break;   // (the whole warp agrees)
-    if ((be & 31) == lane) open &= ~(1u << (be >> 5));
-    if (lane == j) my_id = be;
   }
   double mine = my_id >= 0 ? score(my_id) : 0.0;
   if (a.renorm) {
@@ -180,6 +201,12 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+// An expert's choice value in fp64 (softmax's would need its sum; not here).
+template <bool BIASED>
+__device__ __forceinline__ double exact_choice(float z, float b) {
+  return BIASED ? 1.0 / (1.0 + exp(-static_cast<double>(z))) + static_cast<double>(b) : static_cast<double>(z);
+}
 
 // What a warp keeps from row to row.
 template <int PL>
@@ -268,7 +295,7 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
       first = fmaxf(first, f);
     }
     const float rank = a.top2 ? first + second : first;
-    int32_t key = g < a.groups ? key_of(rank) : kNone;
+    int32_t key = g < a.groups ? key_of(rank + 0.0f) : kNone;
     int32_t last = 0;
     kept = 0;
     for (int r = 0; r < a.keep; ++r) {
@@ -288,7 +315,7 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
   int32_t key[PL];
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
-    key[i] = (key_of(v[i]) & ~(PL - 1)) | (PL - 1 - i);
+    key[i] = (key_of(v[i] + 0.0f) & ~(PL - 1)) | (PL - 1 - i);   // (-0 is 0)
     if (lane + 32 * i >= a.experts || !((kept >> l.group_of(i)) & 1u)) key[i] = kNone;
     second = max(second, min(first, key[i]));
     first = max(first, key[i]);
@@ -320,18 +347,51 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
     }
   }
   const bool got = lane <= a.topk && taken != kNone;
-  const int id = from + 32 * (PL - 1 - (taken & (PL - 1)));
-  const float z = got ? load_logit(zt + id) : 0.0f;
+  int id = from + 32 * (PL - 1 - (taken & (PL - 1)));
+  float z = got ? load_logit(zt + id) : 0.0f;
   {
     const float b = got && BIASED ? __ldg(a.bias + id) : 0.0f;
     const float mine = value_of(taken & ~(PL - 1)), next = __shfl_down_sync(kAll, mine, 1);
     const int32_t next_key = __shfl_down_sync(kAll, taken, 1);
-    const float room = BIASED ? 2.0f * kErr + fmaxf(fabsf(mine), fabsf(next)) * ((PL + 2) * 0x1p-23f) : 0.0f;
-    bool near = lane < a.topk && next_key != kNone && mine - next <= room;
+    auto room = [&](float x, float y) {
+      return BIASED ? 2.0f * kErr + fmaxf(fabsf(x), fabsf(y)) * ((PL + 2) * 0x1p-23f) : 0.0f;
+    };
+    bool near = lane < a.topk && next_key != kNone && mine - next <= room(mine, next);
+    const bool last = (__ballot_sync(kAll, near) >> (a.topk - 1)) & 1u;
+    if (last) {   // the last place is in question: is it between these two?
+      const int32_t rest = __reduce_max_sync(kAll, first);
+      const float edge = __shfl_sync(kAll, mine, a.topk - 1), out = value_of(rest & ~(PL - 1));
+      if (rest != kNone && edge - out <= room(edge, out)) return false;
+    }
     if (__any_sync(kAll, near)) {   // near, but not the same
       const float nz = __shfl_down_sync(kAll, z, 1), nb = __shfl_down_sync(kAll, b, 1);
       near = near && !(z == nz && b == nb);
-      if (__any_sync(kAll, near)) return false;
+    }
+    const uint32_t nears = __ballot_sync(kAll, near);
+    if (nears) {   // the keys taken are ranked again by their values in fp64
+      if (!SIGMOID && BIASED) return false;
+      const double c = got ? exact_choice<BIASED>(z, b) : 0.0;
+      const int n = a.topk + (last ? 1 : 0);
+      int place = 0;
+      for (int o = 0; o < n; ++o) {
+        const double oc = __shfl_sync(kAll, c, o);
+        const int oid = __shfl_sync(kAll, id, o);
+        const bool is = __shfl_sync(kAll, static_cast<int>(got), o) != 0;
+        place += is && (oc > c || (oc == c && oid < id)) ? 1 : 0;
+      }
+      if (!got || lane >= n) place = lane;
+      int new_id = id;
+      float new_z = z;
+      for (int o = 0; o < n; ++o) {
+        const int at = __shfl_sync(kAll, place, o), oid = __shfl_sync(kAll, id, o);
+        const float oz = __shfl_sync(kAll, z, o);
+        if (at == lane) {
+          new_id = oid;
+          new_z = oz;
+        }
+      }
+      id = new_id;
+      z = new_z;
     }
   }
   float s = 0.0f;
@@ -347,15 +407,11 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
   return true;
 }
 
-// PL: experts per lane (a power of two).
-template <typename T, int PL, bool SIGMOID, bool BIASED>
-__global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 8 : PL == 16 ? 6 : 4)
-    router_scored_kernel(const __grid_constant__ RouterArgs a) {
-  // a double per expert, or a float per expert and up to 31 between two groups
-  constexpr int kSpace = PL * 64 > PL * 32 + 1024 ? PL * 64 : PL * 32 + 1024;
-  __shared__ alignas(8) float s_space[kWarps][kSpace];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Lane<PL> l;
+// One row by the whole warp, out of line: by fast_row, else by slow_row.
+// `space`: a double per expert and 4 KB.
+template <typename T, int PL>
+__device__ __forceinline__ void lane_of(const RouterArgs& a, bool biased, Lane<PL>& l) {
+  const int lane = threadIdx.x & 31;
   bool plain = true;
 #pragma unroll
   for (int i = 0; i < (PL + 3) / 4; ++i) l.group[i] = 0;
@@ -366,11 +422,386 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 8 : PL == 16 ? 6 : 4)
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 32 * i;
-    l.bias[i] = BIASED && e < a.experts ? __ldg(a.bias + e) : 0.0f;
+    l.bias[i] = biased && e < a.experts ? __ldg(a.bias + e) : 0.0f;
     plain = plain && fabsf(l.bias[i]) < INFINITY;
     if (a.keep < a.groups && e < a.experts) l.group[i >> 2] |= static_cast<uint32_t>(e / l.size) << (8 * (i & 3));
   }
   l.plain = __all_sync(0xFFFFFFFFu, plain);
+}
+template <typename T, bool SIGMOID, bool BIASED>
+__device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plain, double* space) {
+  bool ok = false;
+  if (plain) {
+    if (a.experts <= 256) {
+      Lane<8> l;
+      lane_of<T, 8>(a, BIASED, l);
+      ok = fast_row<T, 8, SIGMOID, BIASED>(a, t, l, reinterpret_cast<float*>(space));
+    } else {
+      Lane<16> l;
+      lane_of<T, 16>(a, BIASED, l);
+      ok = fast_row<T, 16, SIGMOID, BIASED>(a, t, l, reinterpret_cast<float*>(space));
+    }
+  }
+  __syncwarp();
+  if (!ok) slow_row<T>(a, t, space);
+}
+
+// ------------------------------------------------------------------ many rows
+// Four threads per token, eight tokens a warp: next to no shuffles and no idle
+// lanes.  The rows lie in shared memory; eight experts at a time are turned
+// into keys, sorted by a network and merged into the thread's eight largest,
+// and the four threads' eights at the end.  The keys' lowest bits hold the
+// expert (all ones minus it), which costs more of the value than fast_row's,
+// so about 2 % of the rows are near ties here; the whole warp does those again
+// by fast_row, and by slow_row where that cannot decide either.
+constexpr int kRowsWarps = 2;
+constexpr int kRowsTopk = 8;
+constexpr int kRowsOf = 8;         // tokens of a warp
+constexpr int kRowsBytes = 1024;   // largest row
+constexpr int kRowsLeast = 256;
+
+__device__ __forceinline__ void order2(int32_t& a, int32_t& b) {
+  const int32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// Batcher's odd-even merge sort of eight, largest first (19 exchanges).
+__device__ __forceinline__ void sort8(int32_t (&k)[8]) {
+  order2(k[0], k[1]), order2(k[2], k[3]), order2(k[4], k[5]), order2(k[6], k[7]);
+  order2(k[0], k[2]), order2(k[1], k[3]), order2(k[4], k[6]), order2(k[5], k[7]);
+  order2(k[1], k[2]), order2(k[5], k[6]);
+  order2(k[0], k[4]), order2(k[1], k[5]), order2(k[2], k[6]), order2(k[3], k[7]);
+  order2(k[2], k[4]), order2(k[3], k[5]);
+  order2(k[1], k[2]), order2(k[3], k[4]), order2(k[5], k[6]);
+}
+// Keeps the eight largest of two sorted eights, sorted; `lost` the largest of the rest.
+__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t& lost) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lost = max(lost, min(top[i], k[7 - i]));
+    top[i] = max(top[i], k[7 - i]);
+  }
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) order2(top[i], top[i + d]);
+}
+
+__device__ __forceinline__ void eight(const float* z, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(z), b = *reinterpret_cast<const float4*>(z + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void eight(const __nv_bfloat16* z, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(z);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ float in_shared(const float* z) { return *z; }
+__device__ __forceinline__ float in_shared(const __nv_bfloat16* z) { return __bfloat162float(*z); }
+
+struct RowsShape {
+  int pieces, stride;   // 16-byte pieces of a row, and from row to row in shared memory
+  int size, mask;       // experts of a group; the key bits that hold the expert
+  int bias_floats, warp_bytes;
+};
+template <typename T>
+__host__ __device__ inline RowsShape rows_shape(const RouterArgs& a) {
+  RowsShape s;
+  s.pieces = a.experts * static_cast<int>(sizeof(T)) / 16;
+  s.stride = s.pieces | 1;
+  s.size = a.experts / a.groups;
+  s.mask = 1;
+  while (s.mask < a.experts) s.mask *= 2;
+  s.mask -= 1;
+  // groups' biases lie 4 floats further apart, so that threads at different groups read different banks
+  s.bias_floats = a.bias ? a.experts + 4 * a.groups : 0;
+  // the rows and their groups' ranks; then, in the same place, what again_row needs
+  const int rows = kRowsOf * (s.stride * 16 + a.groups * 4), again = a.experts * 8 + 4096;
+  s.warp_bytes = rows > again ? rows : again;
+  return s;
+}
+
+template <typename T, bool SIGMOID, bool BIASED>
+__global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const __grid_constant__ RouterArgs a) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  extern __shared__ uint4 s_rows[];
+  const RowsShape sh = rows_shape<T>(a);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3, own = lane >> 2;
+  float* s_bias = reinterpret_cast<float*>(s_rows);
+  uint8_t* mine = reinterpret_cast<uint8_t*>(s_rows) + sh.bias_floats * 4 + warp * sh.warp_bytes;
+  uint4* tile = reinterpret_cast<uint4*>(mine);
+  float* s_rank = reinterpret_cast<float*>(mine + kRowsOf * sh.stride * 16) + own;   // [group][token]
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRowsWarps + warp) * kRowsOf;
+  const int rows = static_cast<int>(a.m - t0 < kRowsOf ? (a.m > t0 ? a.m - t0 : 0) : kRowsOf);
+  {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + t0 * a.experts);
+    int row = 0, at = lane;
+    while (at >= sh.pieces) at -= sh.pieces, ++row;
+#pragma unroll 4
+    for (int i = lane; i < rows * sh.pieces; i += 32) {
+      const uint32_t to = smem_u32(tile + row * sh.stride + at);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + i) : "memory");
+      at += 32;
+      while (at >= sh.pieces) at -= sh.pieces, ++row;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  bool plain = true;
+  if (BIASED)
+    for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
+      const float b = __ldg(a.bias + e);
+      s_bias[e + 4 * (e / sh.size)] = b;
+      plain = plain && fabsf(b) < INFINITY;
+    }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  plain = __syncthreads_and(plain);
+  if (rows == 0) return;
+  const T* z = reinterpret_cast<const T*>(tile + own * sh.stride);
+  const bool grouped = a.keep < a.groups;
+  bool done = plain && own < rows;   // decided here
+  float top2 = 0.0f, inv = 1.0f;
+  if (!SIGMOID) {
+    float top = -INFINITY;
+    for (int e = 8 * sub; e < a.experts; e += 32) {
+      float v[8];
+      eight(z + e, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i]);
+    }
+    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+    top2 = fmaxf(top, __shfl_xor_sync(kAll, top, 2)) * kLog2e;
+    if (BIASED || !a.renorm || (grouped && a.top2)) {
+      float sum[2] = {0.0f, 0.0f};
+      for (int e = 8 * sub; e < a.experts; e += 32) {
+        float v[8];
+        eight(z + e, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i & 1] += ex2(fmaf(v[i], kLog2e, -top2));
+      }
+      float all = sum[0] + sum[1];
+      all += __shfl_xor_sync(kAll, all, 1);
+      inv = rcp(all + __shfl_xor_sync(kAll, all, 2));
+    }
+  }
+  // (a sum's chain is at most 64 + 3 adds, each relative 2^-24)
+  constexpr float kErr = SIGMOID ? 5e-7f : 80 * 0x1p-24f;
+  auto score = [&](float x) { return SIGMOID ? rcp(1.0f + ex2(x * -kLog2e)) : ex2(fmaf(x, kLog2e, -top2)) * inv; };
+  uint32_t kept = 0;
+  if (grouped) {
+    for (int g = 0; g < a.groups; ++g) {
+      float first = -INFINITY, second = -INFINITY;
+      for (int j = 8 * sub; j < sh.size; j += 32) {
+        float v[8];
+        eight(z + g * sh.size + j, v);
+        // beyond 40 an fp32 weight may underflow where its fp64 form does not
+#pragma unroll
+        for (int i = 0; i < 8; ++i) done = done && fabsf(v[i]) < 40.0f;   // (not of a NaN)
+        if (BIASED || a.top2) {
+          float b[8];
+          if (BIASED) eight(s_bias + g * (sh.size + 4) + j, b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = BIASED ? score(v[i]) + b[i] : score(v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          second = fmaxf(second, fminf(first, v[i]));
+          first = fmaxf(first, v[i]);
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const float f = __shfl_xor_sync(kAll, first, o), s = __shfl_xor_sync(kAll, second, o);
+        second = fmaxf(fminf(first, f), fmaxf(second, s));
+        first = fmaxf(first, f);
+      }
+      if (sub == 0) s_rank[g * kRowsOf] = a.top2 ? first + second : first;
+    }
+    __syncwarp();
+    float in = INFINITY, out = -INFINITY;
+    for (int g = sub; g < a.groups; g += 4) {
+      const float r = s_rank[g * kRowsOf];
+      int better = 0;
+#pragma unroll 4
+      for (int o = 0; o < a.groups; ++o) {
+        const float other = s_rank[o * kRowsOf];
+        better += (other > r || (other == r && o < g)) ? 1 : 0;
+      }
+      if (better < a.keep) {
+        kept |= 1u << g;
+        in = fminf(in, r);
+      } else {
+        out = fmaxf(out, r);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      kept |= __shfl_xor_sync(kAll, kept, o);
+      in = fminf(in, __shfl_xor_sync(kAll, in, o));
+      out = fmaxf(out, __shfl_xor_sync(kAll, out, o));
+    }
+    if (BIASED || a.top2) done = done && in - out > 4.0f * kErr + 0x1p-21f * fmaxf(fabsf(in), fabsf(out));
+  } else {
+    kept = (a.groups == 32 ? 0u : 1u << a.groups) - 1u;
+  }
+  int32_t top[8], lost = kNone;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = kNone;
+  bool empty = true;
+  for (int n = 0; n < a.keep; ++n) {
+    const int g = kept ? __ffs(kept) - 1 : 0;   // (a row that holds a NaN may have kept fewer; it is not done here)
+    kept &= kept - 1;
+    for (int j = 8 * sub; j < sh.size; j += 32) {
+      const int e = g * sh.size + j;
+      float v[8], b[8];
+      eight(z + e, v);
+      if (BIASED) eight(s_bias + e + 4 * g, b);
+      int32_t k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!grouped) done = done && fabsf(v[i]) < 40.0f;
+        const float c = BIASED ? score(v[i]) + b[i] : v[i] + 0.0f;   // (-0 is 0)
+        k[i] = (key_of(c) & ~sh.mask) | (sh.mask - e - i);
+      }
+      sort8(k);
+      if (empty) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = k[i];
+        empty = false;
+      } else {
+        merge8(top, k, lost);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    int32_t k[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(kAll, top[i], o);
+    lost = max(lost, __shfl_xor_sync(kAll, lost, o));
+    merge8(top, k, lost);
+  }
+  // thread `sub` of the four has the choices sub and sub + 4
+  int id[2];
+  bool close[2] = {false, false};
+  auto room = [&](float x, float y) {
+    return BIASED ? 2.0f * kErr + fmaxf(fabsf(x), fabsf(y)) * ((sh.mask + 3) * 0x1p-23f) : 0.0f;
+  };
+  auto expert = [&](int32_t key) { return min(sh.mask - (key & sh.mask), a.experts - 1); };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int32_t key = top[4 * h], after = top[4 * h + 1];
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      if (sub == i) {
+        key = top[4 * h + i];
+        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost;
+      }
+    id[h] = expert(key);
+    if (BIASED || sizeof(T) == 4) {   // (a bf16 logit's key holds all of it)
+      const float hi = value_of(key & ~sh.mask), lo = value_of(after & ~sh.mask);
+      close[h] = sub + 4 * h < a.topk && after != kNone && !(hi - lo > room(hi, lo));
+    }
+  }
+  if (BIASED || sizeof(T) == 4) {
+    const uint32_t quad = 15u << (lane & ~3);
+    const uint32_t c0 = __ballot_sync(kAll, close[0] && done), c1 = __ballot_sync(kAll, close[1] && done);
+    if (!SIGMOID && BIASED) {   // (softmax's fp64 sum is slow_row's)
+      if ((c0 | c1) & quad) done = false;
+    } else if (c0 | c1) {
+      // Near ties: the choices and the next expert ranked again by their values
+      // in fp64.  Where the last place is in question, no other expert may be
+      // near it.
+      const int edge = a.topk - 1;
+      const bool last = (((edge < 4 ? c0 : c1) & quad) >> ((lane & ~3) + (edge & 3))) & 1u;
+      int32_t at_edge = top[0], beyond = kNone;
+      int next_id = expert(lost);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i == edge) at_edge = top[i];
+        if (i == a.topk) next_id = expert(top[i]);
+        if (i == a.topk + 1) beyond = top[i];
+      }
+      if (a.topk == 7) beyond = lost;
+      const float e0 = value_of(at_edge & ~sh.mask), e1 = value_of(beyond & ~sh.mask);
+      // (with eight choices the expert after the next is not known)
+      if (last && (a.topk == 8 || (beyond != kNone && !(e0 - e1 > room(e0, e1))))) done = false;
+      // the next expert, at place topk, is every thread's; choices past topk count for nothing
+      auto value = [&](int e) {
+        return exact_choice<BIASED>(in_shared(z + e), BIASED ? s_bias[e + 4 * (e / sh.size)] : 0.0f);
+      };
+      const double c[2] = {value(id[0]), value(id[1])}, cn = value(next_id);
+      int place[2] = {0, 0}, place_n = 0;
+      for (int o = 0; o < a.topk; ++o) {
+        const int from = (lane & ~3) | (o & 3);
+        const double oc = __shfl_sync(kAll, o < 4 ? c[0] : c[1], from);
+        const int oid = __shfl_sync(kAll, o < 4 ? id[0] : id[1], from);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) place[h] += (oc > c[h] || (oc == c[h] && oid < id[h])) ? 1 : 0;
+        place_n += (oc > cn || (oc == cn && oid < next_id)) ? 1 : 0;
+      }
+      if (last)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) place[h] += (cn > c[h] || (cn == c[h] && next_id < id[h])) ? 1 : 0;
+      int new_id[2] = {id[0], id[1]};
+      for (int o = 0; o < a.topk; ++o) {
+        const int from = (lane & ~3) | (o & 3);
+        const int at = __shfl_sync(kAll, o < 4 ? place[0] : place[1], from);
+        const int oid = __shfl_sync(kAll, o < 4 ? id[0] : id[1], from);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (at == sub + 4 * h) new_id[h] = oid;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) id[h] = last && place_n == sub + 4 * h ? next_id : new_id[h];
+    }
+  }
+  float w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = 0.0f;
+    if (sub + 4 * h < a.topk) {
+      const float x = in_shared(z + id[h]);
+      w[h] = SIGMOID ? rcp(1.0f + expf(-x)) : ex2(fmaf(x, kLog2e, -top2)) * inv;
+    }
+  }
+  if (a.renorm) {   // summed in the order of fast_row's shuffles: the same bits
+    float total = w[0] + w[1];
+    total += __shfl_xor_sync(kAll, total, 2);
+    const float f = rcp(total + __shfl_xor_sync(kAll, total, 1));
+    w[0] *= f;
+    w[1] *= f;
+  }
+  const uint32_t undone = __ballot_sync(kAll, !done && own < rows);   // (no thread needs the rows any more)
+  const bool redo = ((undone >> (lane & ~3)) & 15u) != 0;
+  if (!redo && own < rows) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (sub + 4 * h < a.topk) {
+        const int64_t at = (t0 + own) * a.topk + sub + 4 * h;
+        a.ids[at] = id[h];
+        a.weights[at] = w[h] * a.scale;
+      }
+  }
+  for (int r = 0; undone >> (4 * r) != 0 && r < rows; ++r)
+    if ((undone >> (4 * r)) & 15u)
+      again_row<T, SIGMOID, BIASED>(a, t0 + r, plain, reinterpret_cast<double*>(mine));
+}
+
+// PL: experts per lane (a power of two).
+template <typename T, int PL, bool SIGMOID, bool BIASED>
+__global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 8 : PL == 16 ? 6 : 4)
+    router_scored_kernel(const __grid_constant__ RouterArgs a) {
+  // a double per expert, or a float per expert and up to 31 between two groups
+  constexpr int kSpace = PL * 64 > PL * 32 + 1024 ? PL * 64 : PL * 32 + 1024;
+  __shared__ alignas(8) float s_space[kWarps][kSpace];
+  const int warp = threadIdx.x >> 5;
+  Lane<PL> l;
+  lane_of<T, PL>(a, BIASED, l);
   // topk + 1 keys are taken, one per lane
   const bool fits = a.topk < 32;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < a.m; t += static_cast<int64_t>(gridDim.x) * kWarps)
@@ -396,7 +827,33 @@ cudaError_t launch_as(const RouterArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 template <typename T>
+bool rows_fit(const RouterArgs& a) {
+  return a.m >= kRowsLeast && a.topk <= kRowsTopk && a.topk < a.keep * (a.experts / a.groups) &&
+         (a.experts / a.groups) % 8 == 0 && a.experts * sizeof(T) <= kRowsBytes && a.experts * sizeof(T) % 16 == 0 &&
+         reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+}
+template <typename T, bool SIGMOID, bool BIASED>
+cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(router_rows_kernel<T, SIGMOID, BIASED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                160 * 1024);
+  });
+  if (e != cudaSuccess) return e;
+  const RowsShape s = rows_shape<T>(a);
+  const int64_t rows = kRowsOf * kRowsWarps;
+  router_rows_kernel<T, SIGMOID, BIASED><<<static_cast<unsigned>((a.m + rows - 1) / rows), kRowsWarps * 32,
+                                           s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st>>>(a);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+template <typename T>
 cudaError_t launch_pl(const RouterArgs& a, cudaStream_t st) {
+  if (rows_fit<T>(a)) {
+    if (a.sigmoid) return a.bias ? launch_rows<T, true, true>(a, st) : launch_rows<T, true, false>(a, st);
+    return a.bias ? launch_rows<T, false, true>(a, st) : launch_rows<T, false, false>(a, st);
+  }
   const int per = (a.experts + 31) / 32;
   if (per <= 4) return launch_as<T, 4>(a, st);
   if (per <= 8) return launch_as<T, 8>(a, st);

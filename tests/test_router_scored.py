@@ -227,6 +227,52 @@ def test_many_rows_and_rows_behind_untouched():
     assert bool((gi[[0, 17]] == -7).all()) and bool((gw[[0, 17]] == -7).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m,E,topk,groups,keep,group_score,with_bias,renorm", [
+    (2048, 256, 8, 8, 4, "top2", True, True),
+    (2079, 256, 8, 8, 4, "top2", False, False),
+    (2081, 128, 6, 1, 1, "max", True, True),
+    (2049, 128, 6, 1, 1, "max", False, True),
+    (2500, 64, 3, 8, 2, "max", False, True),         # groups of 8, logits alone
+    (2100, 512, 8, 32, 1, "top2", True, False),      # the widest bf16 row; one group of 16
+    (2100, 24, 1, 1, 1, "max", True, True),
+    (2100, 64, 8, 8, 8, "max", True, True),          # every group kept
+])
+def test_many_rows_match_plain(m, E, topk, groups, keep, group_score, with_bias, renorm, score, dtype):
+    z = logits(m, E, m + E, dtype)
+    z[5] = 0.0                                       # all equal
+    z[6, ::2] = -0.0                                 # zeros of both signs are equal
+    z[6, 1::2] = 0.0
+    z[7] *= 100.0
+    z[40] -= 300.0
+    z[41, E // 2:] = -np.inf
+    b = bias_of(E, E) if with_bias else None
+    check(z, topk, b, score, groups, keep, group_score, renorm, 2.5)
+    assert tq.tq4_1s_get_status() == 0
+    z[m - 1, E - 1] = np.nan                         # in a group that may be left out
+    z[100, 0] = np.inf
+    check(z, topk, b, score, groups, keep, group_score, renorm)
+    assert tq.tq4_1s_get_status() == tq.TQ_DEV_NONFINITE
+    if with_bias:                                    # equal biases: ties by id wherever logits are equal
+        check(z[:m - 1], topk, torch.zeros(E), score, groups, keep, group_score, renorm)
+        b[3], b[5] = -np.inf, np.nan
+        check(z[:m - 1], topk, b, score, groups, keep, group_score, renorm)
+
+
+@pytest.mark.gpu
+def test_zeros_of_both_signs_are_equal():
+    z = torch.zeros(4, 64, device=DEV)
+    z[0, ::2] = -0.0
+    z[1, 1::3] = -0.0
+    z[2, :] = -0.0
+    for score in ("softmax", "sigmoid"):
+        check(z, 9, None, score)
+        check(z, 9, None, score, 8, 3, "max")
+        check(z, 9, torch.zeros(64), score, 8, 3, "top2")
+
+
 def test_refusals():
     lib = tq.load_library()
     good, null = 4096, None
@@ -267,3 +313,23 @@ def test_refusals_of_the_binding():
     for kw in (dict(topk=0), dict(topk=65), dict(topk=4, num_groups=3), dict(topk=9, num_groups=8, topk_groups=1)):
         with pytest.raises(tq.TQ4Error):
             tq.tq4_1s_router_scored(z, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [60, 3000])
+@pytest.mark.parametrize("topk", [1, 5, 7, 8])
+def test_near_ties_of_many_rows(m, topk):
+    # logits on a coarse grid and biases that differ by 2^-20 .. 2^-26: most rows have neighbours that fp32 cannot order
+    E = 64
+    rng = np.random.default_rng(m + topk)
+    z = (rng.integers(-6, 7, (m, E)) / 4).astype(np.float32)
+    b = (rng.integers(0, 3, E) * 0.125 + rng.integers(-8, 9, E) * 2.0 ** -rng.integers(20, 27, E)).astype(np.float32)
+    zt = torch.from_numpy(z).to(DEV)
+    for score in ("sigmoid", "softmax"):
+        check(zt, topk, torch.from_numpy(b), score)
+        check(zt, topk, torch.from_numpy(b), score, 8, 3, "top2")
+        check(zt.bfloat16(), topk, torch.from_numpy(b), score, 4, 2, "max")
+    # logits alone, a unit or two apart
+    z = (z.view(np.int32) + rng.integers(0, 3, z.shape).astype(np.int32) * (z != 0)).view(np.float32)
+    check(torch.from_numpy(z).to(DEV), topk, None, "sigmoid", 8, 3, "max")
+    check(torch.from_numpy(z).to(DEV), topk, None, "softmax")
