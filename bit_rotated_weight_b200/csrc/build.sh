@@ -9,5 +9,5 @@ NVCC="${NVCC:-nvcc}"
   -gencode arch=compute_100a,code=sm_100a \
   -I"$ROOT/include" -I"$HERE" \
   "$HERE/tq4_api.cu" "$HERE/tq4_kernels.cu" "$HERE/tq4_streamk.cu" "$HERE/tq4_decode.cu" "$HERE/tq4_gemm.cu" "$HERE/tq4_static.cu" \
-  "$HERE/tq4_router.cu" "$HERE/tq4_int8.cu" "$HERE/tq4_int8_gemm.cu" \
+  "$HERE/tq4_router.cu" "$HERE/tq4_int8.cu" "$HERE/tq4_int8_gemm.cu" "$HERE/tq4_int8_stream.cu" \
   -o "$OUT" ${TQ_EXTRA_NVCC_FLAGS:-}

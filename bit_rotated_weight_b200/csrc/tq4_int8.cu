@@ -8,7 +8,7 @@
 // would round by chance there.
 #include <type_traits>
 
-#include "tq4_int8.h"
+#include "tq4_int8_rows.cuh"
 
 #define TQ_API extern "C" __attribute__((visibility("default")))
 
@@ -30,55 +30,6 @@ __device__ __forceinline__ float to_f32<__half>(__half v) {
   return __half2float(v);
 }
 
-// A row's divisor.  `lift` is a power of two that takes rows of tiny values
-// into the range where 127 / max|x| is finite; it changes no quotient.
-struct RowUnit {
-  float top, recip, lift, scale;
-  bool finite;
-  __device__ __forceinline__ explicit RowUnit(uint32_t top_bits) {
-    finite = top_bits < 0x7F800000u;
-    const float t = __uint_as_float(top_bits);
-    scale = finite ? __fdiv_rn(t, 127.0f) : __uint_as_float(0x7FC00000u);
-    lift = t < 1e-18f ? 0x1p64f : 1.0f;
-    top = t * lift;
-    recip = (finite && t > 0.0f) ? __fdiv_rn(127.0f, top) : 0.0f;
-  }
-};
-
-// The codes of N values, as bytes.  v * recip is within 127 * 2^-23 (1.6e-5)
-// of the real quotient (two roundings of relative 2^-24).  Adding 1.5 * 2^23
-// rounds it to a whole number, ties to even, whose low byte is the code; where
-// it lies within 2e-5 of a border, 127 v is compared with border * top, both
-// exact in 64 bits (31 and 32 significant bits).
-template <int N>
-__device__ __forceinline__ void codes_of(const RowUnit& u, const float (&v)[N], uint32_t (&bytes)[N / 4]) {
-  constexpr float kMagic = 12582912.0f;
-  uint32_t r[N];
-  float worst = 0.0f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float p = __fmul_rn(v[i], u.recip);
-    const float m = __fadd_rn(p, kMagic);
-    r[i] = __float_as_uint(m);
-    worst = fmaxf(worst, fabsf(__fsub_rn(p, __fsub_rn(m, kMagic))));
-  }
-  if (worst > 0.49998f) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float q = __uint_as_float(r[i]) - kMagic, d = __fmul_rn(v[i], u.recip) - q;
-      if (fabsf(d) <= 0.49998f) continue;
-      const float border = q + copysignf(0.5f, d);
-      const double l = 127.0 * static_cast<double>(v[i]), e = static_cast<double>(border) * static_cast<double>(u.top);
-      r[i] = __float_as_uint((l > e ? border + 0.5f : l < e ? border - 0.5f : rintf(border)) + kMagic);
-    }
-  }
-  if (!u.finite)   // (0 * inf and NaN end here)
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = 0;
-#pragma unroll
-  for (int i = 0; i < N; i += 4) bytes[i / 4] = prmt(prmt(r[i], r[i + 1], 0x0040), prmt(r[i + 2], r[i + 3], 0x0040), 0x5410);
-}
-
 struct RowsArgs {
   const void* x;
   int64_t ldx, k, rows;
@@ -88,66 +39,18 @@ struct RowsArgs {
   int32_t* counters;         // zeroed by block 0 (the split product's), or nullptr
   int32_t ncounters;
   // scatter: row t goes to the sorted rows of its topk slots, whose slot
-  // numbers are left in pairs; each expert's next row is cursor[expert].
+  // numbers and weights are left in pairs and row_w; each expert's next row is
+  // cursor[expert].  (The order of an expert's rows may differ from run to
+  // run; a row's results do not depend on its place.)
   const int32_t* ids;
   int32_t topk, num_experts;
   int32_t* cursor;
   int32_t* pairs;
+  const float* topk_w;
+  float* row_w;
 };
 
 constexpr int kRowThreads = 256;
-
-// 16 bytes of a row as fp32, and the largest |v| in them, as fp32 bits.  Bits
-// without the sign order like the values do, NaN and infinities on top, so the
-// maximum of 16-bit types is taken on pairs before any conversion.
-template <typename T>
-struct Vec;
-template <>
-struct Vec<float> {
-  static constexpr int N = 4;
-  static __device__ __forceinline__ uint32_t top(const uint4& r) {
-    return max(max(r.x & 0x7FFFFFFFu, r.y & 0x7FFFFFFFu), max(r.z & 0x7FFFFFFFu, r.w & 0x7FFFFFFFu));
-  }
-  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) { return t; }
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[4]) {
-    v[0] = __uint_as_float(r.x), v[1] = __uint_as_float(r.y), v[2] = __uint_as_float(r.z), v[3] = __uint_as_float(r.w);
-  }
-};
-struct Vec16 {
-  static constexpr int N = 8;
-  static __device__ __forceinline__ uint32_t top(const uint4& r) {
-    const uint32_t m = 0x7FFF7FFFu;
-    const uint32_t t = __vmaxu2(__vmaxu2(r.x & m, r.y & m), __vmaxu2(r.z & m, r.w & m));
-    return max(t & 0xFFFFu, t >> 16);
-  }
-};
-template <>
-struct Vec<__nv_bfloat16> : Vec16 {
-  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) { return t << 16; }
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-};
-template <>
-struct Vec<__half> : Vec16 {
-  static __device__ __forceinline__ uint32_t top_f32(uint32_t t) {
-    return __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(t))));
-  }
-  static __device__ __forceinline__ void unpack(const uint4& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-};
 
 // The destination rows of a scattered row (one expert slot each).
 // `threads` threads work on the row; topk (up to 64) may be more.
@@ -159,6 +62,7 @@ __device__ __forceinline__ void take_rows(const RowsArgs& a, int64_t row, int la
     if (e >= 0 && e < a.num_experts) {
       at = atomicAdd(a.cursor + e, 1);
       a.pairs[at] = static_cast<int32_t>(slot);
+      a.row_w[at] = __ldg(a.topk_w + slot);
     }
     s_at[j] = at;
   }
@@ -351,15 +255,19 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restri
 
 // Counts each expert's slots and writes the segments (at most `chunk` rows of
 // one expert), their number, the number of rows, and each expert's first row
-// (the scatter's cursors).  One block: the slots are few bytes.
+// (the scatter's cursors).  With `pairs` the rows are given out here: the slot
+// and weight of each sorted row.  One block: the slots are few bytes.
 __global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __restrict__ ids, int64_t slots,
                                                              int32_t num_experts, int32_t chunk,
                                                              int32_t* __restrict__ cursor, int4* __restrict__ segs,
-                                                             int32_t* __restrict__ nseg, int32_t* __restrict__ nrows) {
+                                                             int32_t* __restrict__ nseg, int32_t* __restrict__ nrows,
+                                                             const float* __restrict__ topk_w,
+                                                             int32_t* __restrict__ pairs, float* __restrict__ row_w) {
   extern __shared__ int32_t count[];
   __shared__ int32_t s_rows[32], s_segs[32];
   __shared__ int32_t s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
   for (int e = tid; e < num_experts; e += 1024) count[e] = 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
@@ -400,6 +308,7 @@ __global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __re
     const int32_t row = before_r + rows - c, seg = before_s + nsegs - ns;
     if (e < num_experts) {
       cursor[e] = row;
+      count[e] = row;
       for (int32_t i = 0; i < ns; ++i) segs[seg + i] = make_int4(e, row + i * chunk, min(chunk, c - i * chunk), 0);
     }
     rows0 += total_r;
@@ -411,6 +320,14 @@ __global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __re
     *nrows = rows0;
     if (s_bad) raise_status(TQ_DEV_BAD_ROUTING);
   }
+  if (pairs)
+    for (int64_t p = tid; p < slots; p += 1024) {
+      const int32_t e = ids[p];
+      if (e < 0 || e >= num_experts) continue;
+      const int32_t at = atomicAdd(&count[e], 1);
+      pairs[at] = static_cast<int32_t>(p);
+      row_w[at] = topk_w[p];
+    }
 }
 
 template <typename T, int TPR, int NV>
@@ -424,8 +341,13 @@ template <typename T>
 cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
   const int64_t nvec = a.k / Vec<T>::N;
   const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % Vec<T>::N == 0;
-  if (wide && nvec <= 32 * 4) return launch_rows_as<T, 32, 4>(a, cfg);
-  if (wide && nvec <= 128 * 4) return launch_rows_as<T, 128, 4>(a, cfg);
+  if (wide && a.rows >= 148 * 8) {   // enough rows for a warp each
+    if (nvec <= 32 * 4) return launch_rows_as<T, 32, 4>(a, cfg);
+    if (nvec <= 32 * 8) return launch_rows_as<T, 32, 8>(a, cfg);
+    if (nvec <= 32 * 16) return launch_rows_as<T, 32, 16>(a, cfg);
+  }
+  if (wide && nvec <= 128) return launch_rows_as<T, 128, 1>(a, cfg);
+  if (wide && nvec <= 256 * 2) return launch_rows_as<T, 256, 2>(a, cfg);
   if (wide && nvec <= 256 * 4) return launch_rows_as<T, 256, 4>(a, cfg);
   if (wide && nvec <= 256 * 8) return launch_rows_as<T, 256, 8>(a, cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
@@ -515,7 +437,7 @@ LinearLayout linear_layout(int64_t m, int64_t k, const Plan& p) {
 }
 
 struct MoeLayout {
-  size_t cursor, segs, nseg, nrows, pairs, xq, xscale, h, hq, hscale, z, total;
+  size_t cursor, segs, nseg, nrows, pairs, row_w, xq, xscale, h, hq, hscale, z, total;
   int nt;
   int64_t slots, maxseg;
 };
@@ -536,6 +458,7 @@ MoeLayout moe_layout(int64_t m, int32_t topk, int64_t experts, int64_t H, int64_
   L.nseg = take(4);
   L.nrows = take(4);
   L.pairs = take(L.slots * 4);
+  L.row_w = take(L.slots * 4);
   L.xq = take(L.slots * H);
   L.xscale = take(L.slots * 4);
   L.h = take(L.slots * I * 2);
@@ -617,9 +540,27 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
   if (take_injected_failure()) return TQ_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  alignas(64) CUtensorMap tw, tx;
+  if (m <= kStreamTokens && int8_stream_fits(w->k) && aligned16(x) && ldx * elem_bytes(dtype) % 16 == 0) {
+    // few tokens: one kernel that streams the weight and quantizes x itself
+    if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128)) return TQ_ERR_CUDA;
+    Int8StreamArgs a{};
+    a.n = static_cast<int32_t>(w->n);
+    a.k = static_cast<int32_t>(w->k);
+    a.m = static_cast<int32_t>(m);
+    a.row_tiles = static_cast<int32_t>(p.row_tiles);
+    a.ksteps = static_cast<int32_t>(p.ksteps);
+    a.mode = INT8_DENSE;
+    a.dtype = dtype;
+    a.parts = int8_stream_parts(p.row_tiles, p.ksteps, sms);
+    a.ldx = ldx;
+    a.x = x;
+    a.wscale = w->wscale;
+    a.y = y;
+    return rc_of(launch_int8_stream(dtype, tw, a, p.row_tiles, sms, st));
+  }
   uint8_t* base = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
-  alignas(64) CUtensorMap tw, tx;
   if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) || !encode_i8_map(&tx, xq, 0, m, w->k, p.nt))
     return TQ_ERR_CUDA;
   RowsArgs r{};
@@ -687,10 +628,43 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
       !encode_i8_map(&td, down->q, E, H, I, 128) || !encode_i8_map(&th, hq, 0, L.slots, I, L.nt))
     return TQ_ERR_CUDA;
 
-  int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(topk_ids, L.slots, static_cast<int32_t>(E), L.nt,
-                                                                    i32(L.cursor), segs, i32(L.nseg), i32(L.nrows));
+  // few rows an expert: the products quantize their rows themselves
+  const bool stream_rows = L.nt == kStreamTokens && int8_stream_fits(H) && int8_stream_fits(I) && aligned16(x);
+  int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(
+      topk_ids, L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
+      stream_rows ? i32(L.pairs) : nullptr, f32(L.row_w));
   note_launches(1);
   if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
+  if (stream_rows) {
+    Int8StreamArgs s{};
+    s.n = static_cast<int32_t>(I);
+    s.k = static_cast<int32_t>(H);
+    s.row_tiles = static_cast<int32_t>(rt_up);
+    s.ksteps = static_cast<int32_t>((H + 127) / 128);
+    s.mode = INT8_UP;
+    s.parts = 1;
+    s.topk = topk;
+    s.ldx = H;
+    s.x = x;
+    s.segs = segs;
+    s.nseg = i32(L.nseg);
+    s.pairs = i32(L.pairs);
+    s.row_w = f32(L.row_w);
+    s.wscale = up->wscale;
+    s.y = base + L.h;
+    if (launch_int8_stream(dtype, tu, s, tiles_up, sms, st) != cudaSuccess) return TQ_ERR_CUDA;
+    s.n = static_cast<int32_t>(H);
+    s.k = static_cast<int32_t>(I);
+    s.row_tiles = static_cast<int32_t>(rt_dn);
+    s.ksteps = static_cast<int32_t>((I + 127) / 128);
+    s.mode = INT8_DOWN;
+    s.ldx = I;
+    s.x = base + L.h;
+    s.wscale = down->wscale;
+    s.y = base + L.z;
+    if (launch_int8_stream(TQ_DTYPE_BF16, td, s, tiles_dn, sms, st) != cudaSuccess) return TQ_ERR_CUDA;
+  } else {
   RowsArgs r{};
   r.x = x;
   r.ldx = r.k = H;
@@ -702,6 +676,8 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   r.num_experts = static_cast<int32_t>(E);
   r.cursor = i32(L.cursor);
   r.pairs = i32(L.pairs);
+  r.topk_w = topk_w;
+  r.row_w = f32(L.row_w);
   if (launch_rows(dtype, r, true, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(I);
@@ -713,7 +689,6 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   a.xscale = f32(L.xscale);
   a.wscale = up->wscale;
   a.y = base + L.h;
-  const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
   if (launch_int8_gemm(tu, tx, a, L.nt, static_cast<int>(tiles_up < sms ? tiles_up : sms), st) != cudaSuccess)
     return TQ_ERR_CUDA;
   RowsArgs g{};
@@ -731,16 +706,30 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   a.xscale = f32(L.hscale);
   a.wscale = down->wscale;
   a.pairs = i32(L.pairs);
-  a.topk_w = topk_w;
+  a.row_w = f32(L.row_w);
   a.y = base + L.z;
   if (launch_int8_gemm(td, th, a, L.nt, static_cast<int>(tiles_dn < sms ? tiles_dn : sms), st) != cudaSuccess)
     return TQ_ERR_CUDA;
+  }
   const int32_t hg = static_cast<int32_t>(H / 4), experts = static_cast<int32_t>(E);
   const unsigned blocks = static_cast<unsigned>((m * hg + 255) / 256);
-  if (dtype == TQ_DTYPE_BF16)
-    int8_combine_kernel<<<blocks, 256, 0, st>>>(f32(L.z), topk_ids, m, topk, hg, experts, static_cast<__nv_bfloat16*>(y));
-  else
-    int8_combine_kernel<<<blocks, 256, 0, st>>>(f32(L.z), topk_ids, m, topk, hg, experts, static_cast<__half*>(y));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const float* z = f32(L.z);
+  const cudaError_t e =
+      dtype == TQ_DTYPE_BF16
+          ? cudaLaunchKernelEx(&cfg, int8_combine_kernel<__nv_bfloat16>, z, topk_ids, m, topk, hg, experts,
+                               static_cast<__nv_bfloat16*>(y))
+          : cudaLaunchKernelEx(&cfg, int8_combine_kernel<__half>, z, topk_ids, m, topk, hg, experts,
+                               static_cast<__half*>(y));
+  if (e != cudaSuccess) return TQ_ERR_CUDA;
   note_launches(1);
   return rc_of(cudaGetLastError());
 }

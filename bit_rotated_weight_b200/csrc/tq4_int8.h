@@ -20,7 +20,7 @@ struct Int8GemmArgs {
   const float* xscale;      // [rows of xq]
   const float* wscale;      // [experts][n]
   const int32_t* pairs;     // down: flat slot of each sorted row
-  const float* topk_w;      // down: router weight of each slot
+  const float* row_w;       // down: router weight of each sorted row
   void* y;                  // dense: y [m][n]; up: h bf16 [rows][n]; down: fp32 [slots][n]
   int32_t* partials;        // split: [grid][2][NT][128]
   int32_t* counters;        // split: [grid], zero at launch
@@ -30,8 +30,34 @@ struct Int8GemmArgs {
 // is 0 (2-D): box 128 bytes x box_rows, 128-byte swizzle, zeros outside.
 bool encode_i8_map(CUtensorMap* m, const int8_t* base, int64_t experts, int64_t rows, int64_t k, int box_rows);
 
+
 // nt: 16, 32, 64, 128 or 256 tokens a tile (the box rows of tx).
 cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int nt, int grid,
                              cudaStream_t st);
+
+// Products of at most 16 tokens a tile that quantize their tokens themselves
+// (tq4_int8_stream.cu).
+constexpr int kStreamTokens = 16;
+struct Int8StreamArgs {
+  int32_t n, k, m;          // weight rows and columns (of one expert); dense: tokens
+  int32_t row_tiles, ksteps;
+  int32_t mode, dtype;      // Int8Mode; type of y (dense), TQ_DTYPE_*
+  int32_t parts;            // CTAs of a cluster that share a row tile's k (dense; 1: none)
+  int32_t topk;             // up: x row of a sorted row = pairs[row] / topk
+  int64_t ldx;
+  const void* x;            // dense: x; up: x; down: h (bf16, sorted rows)
+  const int4* segs;         // grouped: (expert, first row, rows <= 16, -)
+  const int32_t* nseg;
+  const int32_t* pairs;
+  const float* row_w;
+  const float* wscale;
+  void* y;                  // as Int8GemmArgs
+};
+// Whether rows of k elements fit (their codes stay in shared memory).
+bool int8_stream_fits(int64_t k);
+// The cluster size for a dense product of row_tiles x ksteps.
+int int8_stream_parts(int64_t row_tiles, int64_t ksteps, int sms);
+cudaError_t launch_int8_stream(int xdtype, const CUtensorMap& tw, const Int8StreamArgs& a, int64_t most_tiles, int sms,
+                               cudaStream_t st);
 
 }  // namespace tq4

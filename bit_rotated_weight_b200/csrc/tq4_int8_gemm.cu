@@ -10,17 +10,20 @@
 //   warp 1     one thread issues tcgen05.mma kind::i8 (K = 32), 4 a stage,
 //              into one of two tensor-memory accumulators;
 //   warp 2     allocates / frees tensor memory;
-//   warps 4-7  epilogue, thread = weight row.
+//   warps 4-   epilogue, thread = weight row; of tiles of 64 tokens or more
+//              two warps share 32 rows, each with half of the tokens (one warp
+//              per scheduler is bound by latency: the down projection of 4096
+//              tokens x 6 of 128 experts took 262 us).
+// A tile that holds fewer than NT tokens multiplies only those, rounded up to 16.
 // With `split` the (tile, 128-byte k step) space is cut evenly over the CTAs;
 // the parts of a cut tile are left as int32 in the workspace and summed by the
 // CTA that finishes last.  Integer sums do not depend on their order, so the
 // result is the same bits whatever the cut.
-#include "tq4_int8.h"
+#include "tq4_int8_mma.cuh"
 
 namespace tq4 {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kRows = 128;       // weight rows of a tile
 constexpr int kStep = 128;       // bytes of k per stage
 constexpr int kABytes = kRows * kStep;
@@ -30,6 +33,9 @@ struct Shape {
   static constexpr int kStageBytes = kABytes + NT * kStep;
   static constexpr int kStages = (200 * 1024) / kStageBytes;
   static constexpr int kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kParts = NT >= 64 ? 2 : 1;   // warps that share 32 rows in the epilogue
+  static constexpr int kEpilogue = 128 * kParts;    // its threads
+  static constexpr int kThreads = 128 + kEpilogue;
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
 };
 
@@ -45,34 +51,9 @@ struct Shared {
   int epi_ok[2];
   int last;
   alignas(16) float sx[2][NT < 32 ? 32 : NT];       // the tile's token scales,
-  alignas(16) float tw[2][NT];       // router weights and
-  alignas(16) int32_t slot[2][NT];   // slots (down only)
+  alignas(16) float tw[2][NT < 32 ? 32 : NT];       // router weights and
+  alignas(16) int32_t slot[2][NT < 32 ? 32 : NT];   // slots (down only)
 };
-
-// kind::i8 instruction descriptor: signed 8-bit A and B, int32 D.
-__host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n) {
-  return (2u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
-}
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t addr = smem_u32(bar);
-  const uint64_t t0 = global_timer();
-  while (!mbar_try_wait(addr, parity)) {
-    if (global_timer() - t0 > TQ_WAIT_NS) {
-      raise_status(TQ_DEV_TIMEOUT);
-      return;
-    }
-  }
-}
 
 // One piece of a CTA's work: k steps [k0, k1) of a tile.
 struct Part {
@@ -188,7 +169,7 @@ __device__ __forceinline__ void store16(uint16_t* y, int64_t n, int row, int row
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ Int8GemmArgs a) {
   using S = Shape<NT>;
@@ -203,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.dfull[i], 1);
-      mbar_init(&sh.dempty[i], 128);
+      mbar_init(&sh.dempty[i], S::kEpilogue);
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
@@ -270,11 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*abortp)   // let the copies in flight land before the CTA leaves
         for (int i = 0; i < S::kStages; ++i)
-          if (armed[i] >= 0) drain_wait(&sh.full[i], static_cast<uint32_t>(armed[i]));
+          if (armed[i] >= 0) int8_drain_wait(&sh.full[i], static_cast<uint32_t>(armed[i]));
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8(kRows, NT);
       Walk w(tiles, a.ksteps, split);
       Part p;
       int li = 0, ti = 0;
@@ -284,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp)) break;
         tc_fence_after();
         const uint32_t d_addr = tmem + db * NT;
+        const uint32_t idesc = idesc_i8(kRows, (place_of<NT>(a, p.tile).ntok + 15) & ~15);
         for (int kk = p.k0; kk < p.k1; ++kk, ++li) {
           const int s = li % S::kStages;
           if (!mbar_wait(&sh.full[s], (li / S::kStages) & 1, abortp)) {
@@ -302,11 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++ti;
       }
       mma_commit(&sh.mma_done);
-      drain_wait(&sh.mma_done, 0);
+      int8_drain_wait(&sh.mma_done, 0);
     }
   } else if (warp >= 4) {
     pdl_wait();   // the scales (and the counters) come from the kernel before
-    const int t = (warp & 3) * 32 + lane;
+    const int t = (warp & 3) * 32 + lane;       // the weight row,
+    const int part = (warp - 4) >> 2;           // and which of its tokens:
+    constexpr int kCols = NT / S::kParts;
+    const int col0 = part * kCols;              // columns [col0, col0 + kCols)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     Walk w(tiles, a.ksteps, split);
     const int32_t tile0 = split ? w.at / a.ksteps : 0;
@@ -316,17 +300,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int db = ti & 1;
       const Place pl = place_of<NT>(a, p.tile);
       // (the buffers of the last tile but one: every thread has left it)
-      for (int j = t; j < NT; j += 128) {
+      {
+        const int j = part * 128 + t;
         const bool in = j < pl.ntok;
-        sh.sx[db][j] = in ? __ldcg(a.xscale + pl.tok0 + j) : 0.0f;
-        if (a.mode == INT8_DOWN) {
-          const int32_t slot = in ? __ldcg(a.pairs + pl.tok0 + j) : 0;
-          sh.slot[db][j] = slot;
-          sh.tw[db][j] = in ? __ldg(a.topk_w + slot) : 0.0f;
+        if (j < NT) {
+          sh.sx[db][j] = in ? __ldcg(a.xscale + pl.tok0 + j) : 0.0f;
+          if (a.mode == INT8_DOWN) {
+            sh.slot[db][j] = in ? __ldcg(a.pairs + pl.tok0 + j) : 0;
+            sh.tw[db][j] = in ? __ldcg(a.row_w + pl.tok0 + j) : 0.0f;
+          }
         }
       }
-      if (t == 0) sh.epi_ok[db] = mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp) ? 1 : 0;
-      named_bar_sync(1, 128);
+      if (t == 0 && part == 0) sh.epi_ok[db] = mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp) ? 1 : 0;
+      named_bar_sync(1, S::kEpilogue);
       if (!sh.epi_ok[db]) break;
       tc_fence_after();
       const int row = pl.row0 + t;
@@ -339,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c_last = w.cta_of(u0 + a.ksteps - 1);
         int32_t* mine = a.partials + static_cast<int64_t>(blockIdx.x * 2 + (tile0 == p.tile ? 0 : 1)) * (kRows * NT) + t;
 #pragma unroll 1
-        for (int c = 0; c < NT; c += 16) {
+        for (int c = col0; c < col0 + kCols; c += 16) {
           uint32_t r[16];
           tmem_ld16(d_addr + c, r);
           tmem_wait_ld();
@@ -348,16 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c + j < pl.ntok) __stcg(mine + (c + j) * kRows, static_cast<int32_t>(r[j]));
         }
         __threadfence();
-        named_bar_sync(1, 128);
-        if (t == 0) sh.last = atomicAdd(a.counters + c_first, 1) == c_last - c_first;
-        named_bar_sync(1, 128);
+        named_bar_sync(1, S::kEpilogue);
+        if (t == 0 && part == 0) sh.last = atomicAdd(a.counters + c_first, 1) == c_last - c_first;
+        named_bar_sync(1, S::kEpilogue);
         finish = sh.last != 0;
         if (finish) __threadfence();
       }
       if (finish) {
         const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < pl.ntok; c += 32) {
+        for (int c = col0; c < min(pl.ntok, col0 + kCols); c += 32) {
           int32_t acc[32];
           {
             uint32_t r0[16], r1[16];
@@ -430,7 +416,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmA
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<NT>::kThreads);
   cfg.dynamicSmemBytes = Shape<NT>::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -1,0 +1,32 @@
+// The int8 tensor-core instruction, shared by the int8 products.
+#pragma once
+#include "tq4_int8.h"
+
+namespace tq4 {
+
+// kind::i8 instruction descriptor: signed 8-bit A and B, int32 D.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void int8_drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t addr = smem_u32(bar);
+  const uint64_t t0 = global_timer();
+  while (!mbar_try_wait(addr, parity)) {
+    if (global_timer() - t0 > TQ_WAIT_NS) {
+      raise_status(TQ_DEV_TIMEOUT);
+      return;
+    }
+  }
+}
+
+}  // namespace tq4

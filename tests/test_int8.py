@@ -573,3 +573,42 @@ def test_refusals_of_the_binding():
         tq.tq4_1s_int8_quantize(torch.zeros(4, 48, device=DEV))
     assert tq.tq4_1s_linear_int8(x[:0], w).shape == (0, 64)
     assert tq.tq4_1s_moe_int8(xm[:0], ids[:0], tw[:0], up, down).shape == (0, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,topk,H,I,m,calls", [
+    (128, 6, 288, 1184, 16, 40),     # several row tiles of two segments a block, calls back to back
+    (12, 4, 2688, 160, 24, 20),      # rows of 21 k steps, up to nine tokens a segment
+    (200, 3, 96, 96, 350, 20),       # more segments than blocks: four or five of them a block
+])
+def test_moe_few_rows_an_expert_back_to_back(E, topk, H, I, m, calls):
+    up, down, ru, rd = moe_weights(E, H, I, 80)
+    ids, tw = routing(m, E, topk, 81)
+    x = torch.randn(m, H, generator=gen(82)).to(BF16)
+    y = check_moe(x, ids, tw, up, down, ru, rd)
+    args = x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(tw).to(DEV), up, down
+    ys = [tq.tq4_1s_moe_int8(*args) for _ in range(calls)]
+    assert all(torch.equal(bits(a), bits(y)) for a in ys)
+    assert tq.tq4_1s_get_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(16, 40000, 2688), (1, 20000, 4096), (7, 2048, 8192), (16, 256, 9216)])
+def test_linear_few_tokens_back_to_back(m, n, k):
+    w, q, s = weight(n, k, 83) if n * k < 1 << 25 else (None, None, None)
+    if w is None:                                       # too large for numpy: three row blocks are compared
+        q = torch.randint(-127, 128, (1, n, k), generator=gen(84), dtype=torch.int8)
+        s = torch.rand(1, n, generator=gen(85)) + 0.5
+        w = tq.Int8Weight(q.to(DEV), s.to(DEV), n, k, 1)
+        rows = torch.cat([torch.arange(0, 140), torch.arange(n // 2, n // 2 + 140), torch.arange(n - 140, n)])
+        q, s = q[:, rows].numpy().astype(np.int64), s[:, rows].numpy()
+    else:
+        rows = torch.arange(n)
+    x = torch.randn(m, k, generator=gen(86)).to(BF16)
+    xd = x.to(DEV)
+    ys = [tq.tq4_1s_linear_int8(xd, w) for _ in range(30)]
+    xq, xs = ref_rows(x)
+    acc = xq.astype(np.float64) @ q[0].T.astype(np.float64)
+    want = torch.from_numpy(ref_fp32(acc, xs, s[0])).to(BF16)
+    assert all(torch.equal(bits(y[:, rows.to(DEV)]), bits(want)) for y in ys)
+    assert tq.tq4_1s_get_status() == 0
