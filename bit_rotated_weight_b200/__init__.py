@@ -523,16 +523,12 @@ _SCORES = {"softmax": TQ_SCORE_SOFTMAX, "sigmoid": TQ_SCORE_SIGMOID}
 _GROUP_SCORES = {"max": TQ_GROUP_MAX, "top2": TQ_GROUP_TOP2}
 
 
-def _on_device(fn):
-    """Run an entry point with its first tensor's device current (the library works on the current device)."""
-    @functools.wraps(fn)
-    def call(first, *args, **kwargs):
-        device = first.device if isinstance(first, torch.Tensor) else first.q.device
-        if device.type != "cuda" or device.index == torch.cuda.current_device():
-            return fn(first, *args, **kwargs)
-        with torch.cuda.device(device):
-            return fn(first, *args, **kwargs)
-    return call
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether a tensor lies on another GPU than the current one (the library works on the current device)."""
+    return t.is_cuda and t.get_device() != _current_device()
 
 
 @functools.lru_cache(maxsize=256)
@@ -545,7 +541,6 @@ def _router_struct(num_experts, topk, score, num_groups, topk_groups, group_scor
                    1 if renormalize else 0, scale)
 
 
-@_on_device
 def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | None = None, score: str = "softmax",
                          num_groups: int = 1, topk_groups: int = 1, group_score: str = "max",
                          renormalize: bool = True, scale: float = 1.0):
@@ -555,33 +550,44 @@ def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | N
     among the ``topk_groups`` best of ``num_groups`` groups (ranked by their best expert, "max", or the sum of
     their two best, "top2"); the weights are the scores of the chosen, renormalised if asked, times ``scale``.
     The outputs are what tq4_1s_moe and tq4_1s_moe_int8 take."""
-    if logits.dim() != 2 or not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16):
+    if _elsewhere(logits):
+        with torch.cuda.device(logits.device):
+            return tq4_1s_router_scored(logits, topk, bias, score, num_groups, topk_groups, group_score, renormalize,
+                                        scale)
+    dtype = logits.dtype
+    if logits.dim() != 2 or not logits.is_cuda or (dtype != torch.float32 and dtype != torch.bfloat16):
         raise ValueError("logits must be a CUDA float32/bfloat16 [m][E] tensor")
     m, E = logits.shape
     logits = logits.contiguous()
+    pb = 0
     if bias is not None:
-        if bias.dtype != torch.float32 or bias.shape != (E,) or bias.device != logits.device:
+        if bias.dtype != torch.float32 or bias.dim() != 1 or bias.shape[0] != E or bias.device != logits.device:
             raise ValueError("bias must be a float32 [E] tensor on the logits' device")
         bias = bias.contiguous()
+        pb = bias.data_ptr()
     cfg = _router_struct(E, topk, score, num_groups, topk_groups, group_score, renormalize, scale)
-    ids = torch.empty((m, max(topk, 0)), dtype=torch.int32, device=logits.device)
-    w = torch.empty((m, max(topk, 0)), dtype=torch.float32, device=logits.device)
-    _check(load_library().tq4_1s_router_scored(_ptr(logits), _DTYPES[logits.dtype], m, ctypes.byref(cfg), _ptr(bias),
-                                               _ptr(ids), _ptr(w), _stream(logits.device)), "router_scored")
+    ids = logits.new_empty((m, max(topk, 0)), dtype=torch.int32)
+    w = logits.new_empty((m, max(topk, 0)), dtype=torch.float32)
+    rc = load_library().tq4_1s_router_scored(logits.data_ptr(), _DTYPES[dtype], m, cfg, pb, ids.data_ptr(),
+                                             w.data_ptr(), _stream(logits.device))
+    if rc:
+        raise TQ4Error(rc, "router_scored")
     return ids, w
 
 
-@dataclass
+@dataclass(frozen=True)
 class Int8Weight:
     """An int8 weight (stack): codes q int8 [E][n][k] and one float32 scale per row, wscale [E][n];
-    the weight is wscale[e][i] * q[e][i][j]."""
+    the weight is wscale[e][i] * q[e][i][j].  The handle is fixed (make a new one for other tensors); the tensors'
+    contents may change."""
     q: torch.Tensor
     wscale: torch.Tensor
     n: int
     k: int
     num_experts: int
 
-    def c_struct(self) -> _Int8Weight:
+    @functools.cached_property
+    def _struct(self) -> _Int8Weight:
         E, n, k = self.num_experts, self.n, self.k
         if self.q.dtype != torch.int8 or self.q.numel() != E * n * k or not self.q.is_contiguous():
             raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
@@ -591,14 +597,23 @@ class Int8Weight:
             raise ValueError("Int8Weight planes must lie on one CUDA device")
         return _Int8Weight(n, k, E, 0, self.q.data_ptr(), self.wscale.data_ptr())
 
+    @functools.cached_property
+    def device(self) -> torch.device:
+        return self.q.device
+
+    def c_struct(self) -> _Int8Weight:
+        return self._struct
+
     @property
     def nbytes(self) -> int:
         return self.q.numel() + self.wscale.numel() * 4
 
 
-@_on_device
 def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
     """Quantize W ([n][k] or [E][n][k], float32, bfloat16 or float16, CUDA, k % 32 == 0) to int8 rows."""
+    if _elsewhere(W):
+        with torch.cuda.device(W.device):
+            return tq4_1s_int8_quantize(W)
     if W.dim() == 2:
         W = W.unsqueeze(0)
     if W.dim() != 3 or not W.is_cuda or W.dtype not in _DTYPES:
@@ -613,9 +628,11 @@ def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
     return out
 
 
-@_on_device
 def tq4_1s_int8_dequantize(w: Int8Weight) -> torch.Tensor:
     """The float32 weight [E][n][k] that w stands for."""
+    if _elsewhere(w.q):
+        with torch.cuda.device(w.q.device):
+            return tq4_1s_int8_dequantize(w)
     st = w.c_struct()
     out = torch.empty((w.num_experts, w.n, w.k), dtype=torch.float32, device=w.q.device)
     _check(load_library().tq4_1s_int8_dequantize(ctypes.byref(st), _ptr(out), _stream(out.device)), "int8_dequantize")
@@ -644,31 +661,38 @@ def _check_workspace(workspace, device):
     return workspace
 
 
-@_on_device
 def tq4_1s_linear_int8(x: torch.Tensor, w: Int8Weight, out: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None) -> torch.Tensor:
     """y = x @ W^T with int8 weights and per-token int8 activations; x [m][k] float32, bfloat16 or float16 (CUDA),
     y of the same dtype.  Rows of x may be strided.  Without a workspace each call allocates its own (so calls on
     different streams, and captured graphs, never share one)."""
-    if x.dim() != 2 or not x.is_cuda or x.dtype not in _DTYPES or x.shape[1] != w.k:
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return tq4_1s_linear_int8(x, w, out, workspace)
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or x.dim() != 2 or not x.is_cuda or x.shape[1] != w.k:
         raise ValueError("x must be a CUDA float32/bfloat16/float16 [m][k] tensor with the weight's k")
-    st = w.c_struct()
+    st = w._struct
     m, device = x.shape[0], x.device
-    if w.q.device != device:
+    if w.device != device:
         raise ValueError("x and the weight must lie on one device")
     ldx = x.stride(0)
     if x.stride(1) != 1 or ldx < w.k:
         x = x.contiguous()
         ldx = w.k
-    out = torch.empty((m, w.n), dtype=x.dtype, device=device) if out is None else _check_out(out, (m, w.n), x.dtype,
-                                                                                            device)
-    if workspace is None:
-        workspace = torch.empty(tq4_1s_linear_int8_workspace(m, w), dtype=torch.uint8, device=device)
-    else:
+    out = x.new_empty((m, w.n)) if out is None else _check_out(out, (m, w.n), x.dtype, device)
+    ws = size = 0
+    if workspace is not None:
         _check_workspace(workspace, device)
-    _check(load_library().tq4_1s_linear_int8(x.data_ptr(), _DTYPES[x.dtype], m, ldx, ctypes.byref(st), out.data_ptr(),
-                                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                             _stream(device)), "linear_int8")
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        need = _linear_int8_bytes(m, w.n, w.k, w.num_experts, device.index)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ws, size = workspace.data_ptr(), need
+    rc = load_library().tq4_1s_linear_int8(x.data_ptr(), dtype, m, ldx, st, out.data_ptr(), ws, size, _stream(device))
+    if rc:
+        raise TQ4Error(rc, "linear_int8")
     return out
 
 
@@ -683,32 +707,35 @@ def tq4_1s_moe_int8_workspace(m: int, topk: int, up: Int8Weight, down: Int8Weigh
                            up.q.device.index)
 
 
-@_on_device
 def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, up: Int8Weight, down: Int8Weight,
                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """tq4_1s_moe with int8 experts: y_t = sum_j w_tj * down_e(bf16(relu(up_e(x_t))^2)), x [m][H] bfloat16 or float16.
 
     ``topk_ids`` and ``topk_w`` [m][topk] come from a router (tq4_1s_router_scored, tq4_1s_router_topk)."""
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return tq4_1s_moe_int8(x, topk_ids, topk_w, up, down, out, workspace)
     if x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float16) or x.shape[1] != up.k:
         raise ValueError("x must be a CUDA bfloat16/float16 [m][H] tensor with the up projection's k")
     m, device = x.shape[0], x.device
     if topk_ids.dim() != 2 or topk_ids.shape[0] != m or topk_w.shape != topk_ids.shape:
         raise ValueError("topk_ids and topk_w must both be [m][topk]")
-    if not (topk_ids.device == topk_w.device == up.q.device == down.q.device == device):
+    if not (topk_ids.device == topk_w.device == up.device == down.device == device):
         raise ValueError("x, the routing and the weights must lie on one device")
-    u, d = up.c_struct(), down.c_struct()
+    u, d = up._struct, down._struct
     x = x.contiguous()
     topk_ids = topk_ids.to(torch.int32).contiguous()
     topk_w = topk_w.to(torch.float32).contiguous()
     topk = topk_ids.shape[1]
-    out = torch.empty((m, up.k), dtype=x.dtype, device=device) if out is None else _check_out(out, (m, up.k), x.dtype,
-                                                                                             device)
+    out = x.new_empty((m, up.k)) if out is None else _check_out(out, (m, up.k), x.dtype, device)
     if workspace is None:
-        workspace = torch.empty(tq4_1s_moe_int8_workspace(m, topk, up, down), dtype=torch.uint8, device=device)
+        size = _moe_int8_bytes(m, topk, (up.n, up.k, up.num_experts), (down.n, down.k, down.num_experts), device.index)
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
         _check_workspace(workspace, device)
-    _check(load_library().tq4_1s_moe_int8(x.data_ptr(), _DTYPES[x.dtype], m, topk_ids.data_ptr(), topk_w.data_ptr(),
-                                          topk, ctypes.byref(u), ctypes.byref(d), out.data_ptr(),
-                                          workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                          _stream(device)), "moe_int8")
+        size = workspace.numel() * workspace.element_size()
+    rc = load_library().tq4_1s_moe_int8(x.data_ptr(), _DTYPES[x.dtype], m, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                        topk, u, d, out.data_ptr(), workspace.data_ptr(), size, _stream(device))
+    if rc:
+        raise TQ4Error(rc, "moe_int8")
     return out

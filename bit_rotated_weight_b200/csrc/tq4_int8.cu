@@ -377,8 +377,9 @@ cudaError_t launch_rows(int dtype, const RowsArgs& a, bool dependent, cudaStream
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int rc_of(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
-int elem_bytes(int dtype) { return dtype == TQ_DTYPE_F32 ? 4 : 2; }
-bool aligned_elem(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(dtype) == 0; }
+bool aligned_elem(const void* p, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (dtype == TQ_DTYPE_F32 ? 4 : 2) == 0;
+}
 bool dtype_ok(int dtype) { return dtype == TQ_DTYPE_F32 || dtype == TQ_DTYPE_BF16 || dtype == TQ_DTYPE_F16; }
 
 int weight_ok(const tq4_1s_int8_weight* w, bool need_ptrs) {
@@ -416,6 +417,9 @@ Plan plan_dense(int64_t m, int64_t n, int64_t k, int sms) {
   p.grid = static_cast<int>(units < sms ? units : sms);
   return p;
 }
+
+// Few tokens: one kernel that streams the weight and quantizes x itself.
+bool streams(int64_t m, int64_t k) { return m <= kStreamTokens && int8_stream_fits(k); }
 
 struct LinearLayout {
   size_t xq, xscale, counters, partials, total;
@@ -519,6 +523,7 @@ TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4
 
 TQ_API size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w) {
   if (m <= 0 || m > (1ll << 24) || weight_ok(w, false) != TQ_OK || w->num_experts != 1) return 0;
+  if (streams(m, w->k)) return 0;
   return linear_layout(m, w->k, plan_dense(m, w->n, w->k, sms_or_default())).total;
 }
 
@@ -535,14 +540,14 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   if ((rc = check_device(&sms))) return rc;
   const Plan p = plan_dense(m, w->n, w->k, sms);
   if (p.row_tiles * p.tok_tiles > INT32_MAX / p.ksteps) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  const bool stream_rows = streams(m, w->k);
   const LinearLayout L = linear_layout(m, w->k, p);
-  if (!ws || ws_bytes < L.total) return TQ_ERR_WORKSPACE;
+  if (!stream_rows && (!ws || ws_bytes < L.total)) return TQ_ERR_WORKSPACE;
   if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
   if (take_injected_failure()) return TQ_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   alignas(64) CUtensorMap tw, tx;
-  if (m <= kStreamTokens && int8_stream_fits(w->k) && aligned16(x) && ldx * elem_bytes(dtype) % 16 == 0) {
-    // few tokens: one kernel that streams the weight and quantizes x itself
+  if (stream_rows) {
     if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128)) return TQ_ERR_CUDA;
     Int8StreamArgs a{};
     a.n = static_cast<int32_t>(w->n);
@@ -629,7 +634,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
     return TQ_ERR_CUDA;
 
   // few rows an expert: the products quantize their rows themselves
-  const bool stream_rows = L.nt == kStreamTokens && int8_stream_fits(H) && int8_stream_fits(I) && aligned16(x);
+  const bool stream_rows = L.nt == kStreamTokens && int8_stream_fits(H) && int8_stream_fits(I);
   int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(
       topk_ids, L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
       stream_rows ? i32(L.pairs) : nullptr, f32(L.row_w));

@@ -78,9 +78,19 @@ template <typename T>
 struct Sixteen {
   static constexpr int kVecs = 16 / Vec<T>::N;
   uint4 raw[kVecs];
-  __device__ __forceinline__ void load(const T* at) {
+  // `wide`: rows lie on 16-byte boundaries
+  __device__ __forceinline__ void load(const T* at, bool wide) {
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4*>(at) + i);
+      for (int i = 0; i < kVecs; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4*>(at) + i);
+    } else {
+      load_narrow(at);
+    }
+  }
+  __device__ __noinline__ void load_narrow(const T* at) {
+    alignas(16) T v[16];
+    for (int i = 0; i < 16; ++i) v[i] = at[i];
+    for (int i = 0; i < kVecs; ++i) raw[i] = reinterpret_cast<const uint4*>(v)[i];
   }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t t = 0;
@@ -295,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     // ---- the tokens' codes
     const int q = threadIdx.x - 256;
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
     bool ok = true;
 #pragma unroll 1
     for (int32_t s = seg0, n = (w.row_tile + w.left + a.row_tiles - 1) / a.row_tiles; n > 0 && w.left > 0; ++s, --n) {
@@ -312,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kHold; ++j) {
         const int c = c0 + i0 + j * tpr;
-        if (c < c1) hold[j].load(x + static_cast<int64_t>(c) * 16);
+        if (c < c1) hold[j].load(x + static_cast<int64_t>(c) * 16, wide);
       }
       if (ok) ok = mbar_wait(&sh.bempty[buf], (turn & 1) ^ 1u, abortp);
 #pragma unroll
@@ -321,9 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = c0 + i0 + kHold * tpr; c < c1; c += 2 * tpr) {
         Sixteen<T> v, u;
-        v.load(x + static_cast<int64_t>(c) * 16);
+        v.load(x + static_cast<int64_t>(c) * 16, wide);
         const int d = c + tpr < c1 ? c + tpr : c;
-        u.load(x + static_cast<int64_t>(d) * 16);
+        u.load(x + static_cast<int64_t>(d) * 16, wide);
         top = max(top, max(v.top(), u.top()));
       }
       // the row's largest: within the warp, then among warps and CTAs
@@ -374,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = c0 + i0 + kHold * tpr; c < c1; c += tpr) {
         Sixteen<T> v;
-        v.load(x + static_cast<int64_t>(c) * 16);
+        v.load(x + static_cast<int64_t>(c) * 16, wide);
         put(c, v);
       }
       fence_proxy_async_smem();

@@ -281,7 +281,7 @@ def test_linear_streams_graphs_and_workspaces():
     for g, xin, y, x in graphs:
         assert torch.equal(bits(y), bits(tq.tq4_1s_linear_int8(x * 6, w)))
     with pytest.raises(tq.TQ4Error) as e:
-        tq.tq4_1s_linear_int8(xs[0], w, workspace=ws[:100])
+        tq.tq4_1s_linear_int8(xs[3], w, workspace=ws[:100])
     assert e.value.code == 4
     assert tq.tq4_1s_get_status() == 0
 
@@ -515,7 +515,9 @@ def test_refusals():
     assert lin(m=0) == 0 and lin(x=None) == 1 and lin(y=None) == 1 and lin(m=-1) == 1 and lin(m=(1 << 24) + 1) == 1
     assert lin(ld=63) == 1 and lin(dt=3) == 1 and lin(w=_w(e=2)) == 1
     assert lin(x=4097) == 2 and lin(x=4098, dt=0) == 2 and lin(y=4104) == 2
-    assert lib.tq4_1s_linear_int8_workspace(16, r(_w(n=4096, k=4096))) >= 16 * 4096
+    assert lib.tq4_1s_linear_int8_workspace(17, r(_w(n=4096, k=4096))) >= 17 * 4096
+    assert lib.tq4_1s_linear_int8_workspace(16, r(_w(n=4096, k=4096))) == 0        # few tokens: none needed
+    assert lib.tq4_1s_linear_int8_workspace(16, r(_w(n=4096, k=16384))) > 0        # rows too long to stay on chip
     for m, w in ((0, _w()), (-1, _w()), (16, _w(k=48)), (16, _w(e=2))):
         assert lib.tq4_1s_linear_int8_workspace(m, r(w)) == 0
     up, dn = _w(n=96, k=64, e=4), _w(n=64, k=96, e=4)
