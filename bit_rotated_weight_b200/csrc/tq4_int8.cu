@@ -36,8 +36,6 @@ struct RowsArgs {
   int8_t* q;                 // [rows][k], or sorted rows (scatter)
   float* scale;
   const int32_t* rows_dev;   // rows past *rows_dev are left alone (nullptr: none)
-  int32_t* counters;         // zeroed by block 0 (the split product's), or nullptr
-  int32_t ncounters;
   // scatter: row t goes to the sorted rows of its topk slots, whose slot
   // numbers and weights are left in pairs and row_w; each expert's next row is
   // cursor[expert].  (The order of an expert's rows may differ from run to
@@ -88,8 +86,6 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_con
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  if (a.counters && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.ncounters; i += kRowThreads) a.counters[i] = 0;
   const int64_t rows = a.rows_dev ? __ldcg(a.rows_dev) : a.rows;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + sub;
   const bool live = row < rows;
@@ -126,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_con
 #pragma unroll
       for (int j = 0; j < V::N; ++j) v[j] *= u.lift;
     uint32_t c[V::N / 4];
-    codes_of(u, v, c);
+    V::codes(u, v, c);
     auto put = [&](int64_t to) {
       uint32_t* q = reinterpret_cast<uint32_t*>(a.q + to * a.k) + static_cast<int64_t>(at) * (V::N / 4);
       if constexpr (V::N == 8) *reinterpret_cast<uint2*>(q) = make_uint2(c[0], c[1]);
@@ -148,8 +144,6 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_any_kernel(const __grid
   __shared__ int32_t s_at[64];
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
-  if (a.counters && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.ncounters; i += kRowThreads) a.counters[i] = 0;
   const int64_t row = blockIdx.x;
   if (a.rows_dev && row >= __ldcg(a.rows_dev)) return;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -171,7 +165,8 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_any_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = to_f32(x[i + j]) * u.lift;
     uint32_t c[1];
-    codes_of(u, v, c);
+    if constexpr (sizeof(T) == 2) codes_of_16(u, v, c);
+    else codes_of_32(u, v, c);
     if (a.ids) {
       for (int j = 0; j < a.topk; ++j)
         if (s_at[j] >= 0) *reinterpret_cast<uint32_t*>(a.q + s_at[j] * a.k + i) = c[0];
@@ -344,7 +339,7 @@ cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
   if (wide && a.rows >= 148 * 8) {   // enough rows for a warp each
     if (nvec <= 32 * 4) return launch_rows_as<T, 32, 4>(a, cfg);
     if (nvec <= 32 * 8) return launch_rows_as<T, 32, 8>(a, cfg);
-    if (nvec <= 32 * 16) return launch_rows_as<T, 32, 16>(a, cfg);
+    if (nvec <= 128 * 4) return launch_rows_as<T, 128, 4>(a, cfg);
   }
   if (wide && nvec <= 128) return launch_rows_as<T, 128, 1>(a, cfg);
   if (wide && nvec <= 256 * 2) return launch_rows_as<T, 256, 2>(a, cfg);
@@ -393,28 +388,32 @@ int weight_ok(const tq4_1s_int8_weight* w, bool need_ptrs) {
   return TQ_OK;
 }
 
-int sms_or_default() {
-  int sms = 148;
-  if (check_device(&sms) != TQ_OK) sms = 148;
-  return sms;
-}
-
-// How a dense product is run: tokens a tile, CTAs, and whether tiles are cut.
+// How a dense product is run: tokens a tile, CTAs.
 struct Plan {
   int nt, grid;
-  bool split;
   int64_t row_tiles, tok_tiles, ksteps;
 };
+// The tile width with the least waves x time of a tile.  A tile's time goes
+// about as 232 + NT (7 us at NT = 32, 8.2 at 128, 12.2 at 256, for k = 4096):
+// small tiles are bound by the latency of a k step, and pay while they fit in
+// one wave (512 x 4096 x 4096: 13.5 us at 128, 16.8 at 256, 19.7 at 64), large
+// ones by the MMAs.
 Plan plan_dense(int64_t m, int64_t n, int64_t k, int sms) {
   Plan p;
-  p.nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 128 ? 128 : 256;
+  int64_t best = INT64_MAX;
+  for (const int nt : {16, 32, 64, 128, 256}) {
+    if (nt == 16 ? m > 16 : nt > 32 && m <= nt / 2) continue;
+    const int64_t tiles = (n + 127) / 128 * ((m + nt - 1) / nt), time = (tiles + sms - 1) / sms * (232 + nt);
+    if (time < best) {
+      best = time;
+      p.nt = nt;
+    }
+  }
   p.row_tiles = (n + 127) / 128;
   p.tok_tiles = (m + p.nt - 1) / p.nt;
   p.ksteps = (k + 127) / 128;
   const int64_t tiles = p.row_tiles * p.tok_tiles;
-  p.split = p.nt <= 128 && tiles < 4 * sms;
-  const int64_t units = p.split ? tiles * p.ksteps : tiles;
-  p.grid = static_cast<int>(units < sms ? units : sms);
+  p.grid = static_cast<int>(tiles < sms ? tiles : sms);
   return p;
 }
 
@@ -422,9 +421,9 @@ Plan plan_dense(int64_t m, int64_t n, int64_t k, int sms) {
 bool streams(int64_t m, int64_t k) { return m <= kStreamTokens && int8_stream_fits(k); }
 
 struct LinearLayout {
-  size_t xq, xscale, counters, partials, total;
+  size_t xq, xscale, total;
 };
-LinearLayout linear_layout(int64_t m, int64_t k, const Plan& p) {
+LinearLayout linear_layout(int64_t m, int64_t k) {
   LinearLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -434,8 +433,6 @@ LinearLayout linear_layout(int64_t m, int64_t k, const Plan& p) {
   };
   L.xq = take(static_cast<size_t>(m) * static_cast<size_t>(k));
   L.xscale = take(static_cast<size_t>(m) * 4);
-  L.counters = take(p.split ? static_cast<size_t>(p.grid) * 4 : 0);
-  L.partials = take(p.split ? static_cast<size_t>(p.grid) * 2 * 128 * p.nt * 4 : 0);
   L.total = off;
   return L;
 }
@@ -448,8 +445,14 @@ struct MoeLayout {
 MoeLayout moe_layout(int64_t m, int32_t topk, int64_t experts, int64_t H, int64_t I) {
   MoeLayout L{};
   L.slots = m * topk;
+  // Rows of a segment, by the mean rows of an expert.  While the weight's
+  // stream bounds the layer the width hardly matters (128 experts, 512 tokens
+  // x 6: 237 us at 64 and 128, 243 at 32, 261 at 256); below one row it is the
+  // launches, and the form without quantizing kernels is shorter (1 token 22.7
+  // us, against 25.2); from 136 on it is the MMAs (4096 tokens: 456 us at 256,
+  // 507 at 128; 2048: 351 and 321).
   const int64_t mean = L.slots / experts;
-  L.nt = mean < 8 ? 16 : mean < 16 ? 32 : mean < 32 ? 64 : mean < 80 ? 128 : 256;
+  L.nt = mean < 1 ? 16 : mean < 40 ? 64 : mean < 136 ? 128 : 256;
   L.maxseg = L.slots / L.nt + (experts < L.slots ? experts : L.slots);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -524,7 +527,7 @@ TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4
 TQ_API size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w) {
   if (m <= 0 || m > (1ll << 24) || weight_ok(w, false) != TQ_OK || w->num_experts != 1) return 0;
   if (streams(m, w->k)) return 0;
-  return linear_layout(m, w->k, plan_dense(m, w->n, w->k, sms_or_default())).total;
+  return linear_layout(m, w->k).total;
 }
 
 TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, const tq4_1s_int8_weight* w, void* y,
@@ -541,7 +544,7 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   const Plan p = plan_dense(m, w->n, w->k, sms);
   if (p.row_tiles * p.tok_tiles > INT32_MAX / p.ksteps) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
   const bool stream_rows = streams(m, w->k);
-  const LinearLayout L = linear_layout(m, w->k, p);
+  const LinearLayout L = linear_layout(m, w->k);
   if (!stream_rows && (!ws || ws_bytes < L.total)) return TQ_ERR_WORKSPACE;
   if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
   if (take_injected_failure()) return TQ_ERR_CUDA;
@@ -575,8 +578,6 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   r.rows = m;
   r.q = xq;
   r.scale = reinterpret_cast<float*>(base + L.xscale);
-  r.counters = p.split ? reinterpret_cast<int32_t*>(base + L.counters) : nullptr;
-  r.ncounters = p.grid;
   if (launch_rows(dtype, r, false, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(w->n);
@@ -584,14 +585,11 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   a.row_tiles = static_cast<int32_t>(p.row_tiles);
   a.tok_tiles = static_cast<int32_t>(p.tok_tiles);
   a.ksteps = static_cast<int32_t>(p.ksteps);
-  a.split = p.split ? 1 : 0;
   a.mode = INT8_DENSE;
   a.dtype = dtype;
   a.xscale = r.scale;
   a.wscale = w->wscale;
   a.y = y;
-  a.partials = reinterpret_cast<int32_t*>(base + L.partials);
-  a.counters = reinterpret_cast<int32_t*>(base + L.counters);
   return rc_of(launch_int8_gemm(tw, tx, a, p.nt, p.grid, st));
 }
 

@@ -13,7 +13,6 @@ struct Int8GemmArgs {
   int32_t row_tiles;        // ceil(n / 128)
   int32_t tok_tiles;        // dense: ceil(m / NT)
   int32_t ksteps;           // ceil(k / 128)
-  int32_t split;            // cut the (tile, k step) space evenly over the CTAs
   int32_t mode, dtype;      // Int8Mode; dense: type of y (TQ_DTYPE_*)
   const int4* segs;         // grouped: (expert, first row, rows <= NT, -), else nullptr
   const int32_t* nseg;      // grouped: how many
@@ -22,8 +21,6 @@ struct Int8GemmArgs {
   const int32_t* pairs;     // down: flat slot of each sorted row
   const float* row_w;       // down: router weight of each sorted row
   void* y;                  // dense: y [m][n]; up: h bf16 [rows][n]; down: fp32 [slots][n]
-  int32_t* partials;        // split: [grid][2][NT][128]
-  int32_t* counters;        // split: [grid], zero at launch
 };
 
 // A tensor map over int8 [experts][rows][k] (3-D), or [rows][k] where experts

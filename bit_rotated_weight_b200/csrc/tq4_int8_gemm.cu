@@ -15,10 +15,9 @@
 //              per scheduler is bound by latency: the down projection of 4096
 //              tokens x 6 of 128 experts took 262 us).
 // A tile that holds fewer than NT tokens multiplies only those, rounded up to 16.
-// With `split` the (tile, 128-byte k step) space is cut evenly over the CTAs;
-// the parts of a cut tile are left as int32 in the workspace and summed by the
-// CTA that finishes last.  Integer sums do not depend on their order, so the
-// result is the same bits whatever the cut.
+// A tile's k is never cut between CTAs: with the parts left in memory and
+// summed by the CTA that ends last, 4096 x 4096 took 20 to 28 us at 32 to 128
+// tokens, against 15 us for half or a quarter as many CTAs with whole tiles.
 #include "tq4_int8_mma.cuh"
 
 namespace tq4 {
@@ -49,56 +48,9 @@ struct Shared {
   uint32_t tmem_base;
   int abort_flag;
   int epi_ok[2];
-  int last;
   alignas(16) float sx[2][NT < 32 ? 32 : NT];       // the tile's token scales,
   alignas(16) float tw[2][NT < 32 ? 32 : NT];       // router weights and
   alignas(16) int32_t slot[2][NT < 32 ? 32 : NT];   // slots (down only)
-};
-
-// One piece of a CTA's work: k steps [k0, k1) of a tile.
-struct Part {
-  int32_t tile, k0, k1;
-};
-
-// Walks a CTA's parts; every role walks the same ones.  Cut evenly, CTA c
-// holds the units [c q + min(c, r), (c+1) q + min(c+1, r)).
-struct Walk {
-  int32_t ksteps, grid, per, rest;
-  bool split;
-  int32_t at, end;   // split: units; else tiles
-  __device__ __forceinline__ Walk(int32_t tiles, int32_t ksteps_, bool split_)
-      : ksteps(ksteps_), grid(static_cast<int32_t>(gridDim.x)), split(split_) {
-    if (split) {
-      per = tiles * ksteps / grid;
-      rest = tiles * ksteps - per * grid;
-      at = first_unit(blockIdx.x);
-      end = first_unit(blockIdx.x + 1);
-    } else {
-      per = rest = 0;
-      at = blockIdx.x;
-      end = tiles;
-    }
-  }
-  __device__ __forceinline__ int32_t first_unit(int32_t cta) const { return cta * per + min(cta, rest); }
-  __device__ __forceinline__ int32_t cta_of(int32_t unit) const {
-    const int32_t big = rest * (per + 1);
-    return unit < big ? unit / (per + 1) : rest + (unit - big) / per;
-  }
-  __device__ __forceinline__ bool next(Part& p) {
-    if (at >= end) return false;
-    if (split) {
-      p.tile = at / ksteps;
-      p.k0 = at - p.tile * ksteps;
-      p.k1 = min(ksteps, p.k0 + end - at);
-      at += p.k1 - p.k0;
-    } else {
-      p.tile = at;
-      p.k0 = 0;
-      p.k1 = ksteps;
-      at += grid;
-    }
-    return true;
-  }
 };
 
 // Where a tile lies: expert, first row of W, first token row and how many.
@@ -176,7 +128,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   __shared__ Shared<NT> sh;
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(&sh.full[i], 1);
@@ -207,35 +159,26 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   // call writes) before its producer waits for the quantized activations.
   if (a.segs) pdl_wait();
   const int32_t tiles = a.segs ? __ldcg(a.nseg) * a.row_tiles : a.row_tiles * a.tok_tiles;
-  const bool split = a.split != 0;
 
   if (warp == 0) {
     if (lane == 0) {
-      int armed[S::kStages];
-#pragma unroll
-      for (int i = 0; i < S::kStages; ++i) armed[i] = -1;
       int early = 0;   // stages whose weight half is already on its way
       if (!a.segs) {
-        Walk w(tiles, a.ksteps, split);
-        Part p;
-        while (early < S::kStages && w.next(p)) {
-          const Place pl = place_of<NT>(a, p.tile);
-          for (int kk = p.k0; kk < p.k1 && early < S::kStages; ++kk, ++early) {
+        for (int tile = blockIdx.x; tile < tiles && early < S::kStages; tile += gridDim.x) {
+          const Place pl = place_of<NT>(a, tile);
+          for (int kk = 0; kk < a.ksteps && early < S::kStages; ++kk, ++early) {
             mbar_arrive_expect_tx(&sh.full[early], S::kStageBytes);
             tma_load_3d(smem + early * S::kStageBytes, &tm_w, &sh.full[early], kk * kStep, pl.row0, pl.expert);
           }
         }
         pdl_wait();
       }
-      Walk w(tiles, a.ksteps, split);
-      Part p;
-      int li = 0;
+      int li = 0, s = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      while (ok && w.next(p)) {
-        const Place pl = place_of<NT>(a, p.tile);
-        for (int kk = p.k0; kk < p.k1; ++kk, ++li) {
-          const int s = li % S::kStages;
-          const uint32_t ph = (li / S::kStages) & 1;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        const Place pl = place_of<NT>(a, tile);
+        for (int kk = 0; kk < a.ksteps; ++kk, ++li) {
           uint8_t* st = smem + s * S::kStageBytes;
           if (li >= early) {
             if (!mbar_wait(&sh.empty[s], ph ^ 1u, abortp)) {
@@ -245,60 +188,71 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
             mbar_arrive_expect_tx(&sh.full[s], S::kStageBytes);
             tma_load_3d(st, &tm_w, &sh.full[s], kk * kStep, pl.row0, pl.expert);
           }
-          armed[s] = static_cast<int>(ph);
           tma_load_2d(st + kABytes, &tm_x, &sh.full[s], kk * kStep, pl.tok0);
+          if (++s == S::kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
       if (*abortp)   // let the copies in flight land before the CTA leaves
-        for (int i = 0; i < S::kStages; ++i)
-          if (armed[i] >= 0) int8_drain_wait(&sh.full[i], static_cast<uint32_t>(armed[i]));
+        for (int i = 0; i < min(li, S::kStages); ++i) {
+          s = s == 0 ? S::kStages - 1 : s - 1;
+          if (s == S::kStages - 1) ph ^= 1u;
+          int8_drain_wait(&sh.full[s], ph);
+        }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      Walk w(tiles, a.ksteps, split);
-      Part p;
-      int li = 0, ti = 0;
-      bool ok = true;
-      while (ok && w.next(p)) {
-        const int db = ti & 1;
-        if (!mbar_wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp)) break;
+    // The whole warp walks, one elected lane issues: values that are the same
+    // in every lane stay in the uniform registers that the MMA takes them
+    // from.
+    int s = 0, ti = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const int db = ti & 1;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp))) break;
+      tc_fence_after();
+      const uint32_t d_addr = tmem + db * NT;
+      const uint32_t idesc = idesc_i8(kRows, (place_of<NT>(a, tile).ntok + 15) & ~15);
+      for (int kk = 0; kk < a.ksteps; ++kk) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[s], ph, abortp));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d_addr = tmem + db * NT;
-        const uint32_t idesc = idesc_i8(kRows, (place_of<NT>(a, p.tile).ntok + 15) & ~15);
-        for (int kk = p.k0; kk < p.k1; ++kk, ++li) {
-          const int s = li % S::kStages;
-          if (!mbar_wait(&sh.full[s], (li / S::kStages) & 1, abortp)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + s * S::kStageBytes);
-          const uint32_t b0 = a0 + kABytes;
+        const uint64_t ad = sdesc_k128(smem_u32(smem + s * S::kStageBytes));
+        const uint64_t bd = sdesc_k128(smem_u32(smem + s * S::kStageBytes + kABytes));
+        if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < kStep / 32; ++q)
-            mma_i8(d_addr, sdesc_k128(a0 + q * 32), sdesc_k128(b0 + q * 32), idesc, (kk > p.k0 || q) ? 1u : 0u);
+            mma_i8(d_addr, ad + q * 2, bd + q * 2, idesc, (kk | q) ? 1u : 0u);   // (32 bytes on: 2 units of 16)
           mma_commit(&sh.empty[s]);
         }
-        if (ok) mma_commit(&sh.dfull[db]);
-        ++ti;
+        __syncwarp();
+        if (++s == S::kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
+      if (ok && elect_one()) mma_commit(&sh.dfull[db]);
+      __syncwarp();
+      ++ti;
+    }
+    if (elect_one()) {
       mma_commit(&sh.mma_done);
       int8_drain_wait(&sh.mma_done, 0);
     }
+    __syncwarp();
   } else if (warp >= 4) {
-    pdl_wait();   // the scales (and the counters) come from the kernel before
+    pdl_wait();   // the scales come from the kernel before
     const int t = (warp & 3) * 32 + lane;       // the weight row,
     const int part = (warp - 4) >> 2;           // and which of its tokens:
     constexpr int kCols = NT / S::kParts;
     const int col0 = part * kCols;              // columns [col0, col0 + kCols)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    Walk w(tiles, a.ksteps, split);
-    const int32_t tile0 = split ? w.at / a.ksteps : 0;
-    Part p;
     int ti = 0;
-    while (w.next(p)) {
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++ti) {
       const int db = ti & 1;
-      const Place pl = place_of<NT>(a, p.tile);
+      const Place pl = place_of<NT>(a, tile);
       // (the buffers of the last tile but one: every thread has left it)
       {
         const int j = part * 128 + t;
@@ -317,86 +271,53 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       tc_fence_after();
       const int row = pl.row0 + t;
       const uint32_t d_addr = tmem + lane_base + db * NT;
-      int32_t c_first = 0, c_last = -1;   // the CTAs that share a cut tile
-      bool finish = true;
-      if (p.k0 > 0 || p.k1 < a.ksteps) {
-        const int32_t u0 = p.tile * a.ksteps;
-        c_first = w.cta_of(u0);
-        c_last = w.cta_of(u0 + a.ksteps - 1);
-        int32_t* mine = a.partials + static_cast<int64_t>(blockIdx.x * 2 + (tile0 == p.tile ? 0 : 1)) * (kRows * NT) + t;
+      const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
 #pragma unroll 1
-        for (int c = col0; c < col0 + kCols; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(d_addr + c, r);
+      for (int c = col0; c < min(pl.ntok, col0 + kCols); c += 32) {
+        int32_t acc[32];
+        {
+          uint32_t r0[16], r1[16];
+          tmem_ld16(d_addr + c, r0);
+          if (NT > 16) tmem_ld16(d_addr + c + 16, r1);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < pl.ntok) __stcg(mine + (c + j) * kRows, static_cast<int32_t>(r[j]));
-        }
-        __threadfence();
-        named_bar_sync(1, S::kEpilogue);
-        if (t == 0 && part == 0) sh.last = atomicAdd(a.counters + c_first, 1) == c_last - c_first;
-        named_bar_sync(1, S::kEpilogue);
-        finish = sh.last != 0;
-        if (finish) __threadfence();
-      }
-      if (finish) {
-        const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
-#pragma unroll 1
-        for (int c = col0; c < min(pl.ntok, col0 + kCols); c += 32) {
-          int32_t acc[32];
-          {
-            uint32_t r0[16], r1[16];
-            tmem_ld16(d_addr + c, r0);
-            if (NT > 16) tmem_ld16(d_addr + c + 16, r1);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              acc[j] = static_cast<int32_t>(r0[j]);
-              acc[16 + j] = NT > 16 ? static_cast<int32_t>(r1[j]) : 0;
-            }
+          for (int j = 0; j < 16; ++j) {
+            acc[j] = static_cast<int32_t>(r0[j]);
+            acc[16 + j] = NT > 16 ? static_cast<int32_t>(r1[j]) : 0;
           }
-          for (int32_t o = c_first; o <= c_last; ++o) {
-            if (o == static_cast<int32_t>(blockIdx.x)) continue;
-            const int32_t* theirs = a.partials + static_cast<int64_t>(o * 2 + (w.first_unit(o) / a.ksteps == p.tile ? 0 : 1)) * (kRows * NT) + t;
+        }
+        float v[32];
+        scale32(sh.sx[db] + c, sw, acc, v);
+        const int left = pl.ntok - c;
+        const int64_t tok = pl.tok0 + c;
+        if (a.mode == INT8_DOWN) {
+          float* z = static_cast<float*>(a.y) + row;
+          if (row < a.n)
+#pragma unroll
+            for (int j = 0; j < (NT < 32 ? NT : 32); ++j)
+              if (j < left) z[static_cast<int64_t>(sh.slot[db][c + j]) * a.n] = __fmul_rn(v[j], sh.tw[db][c + j]);
+        } else if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F32) {
+          float* y = static_cast<float*>(a.y) + tok * a.n + row;
+          if (row < a.n)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (j < NT && c + j < pl.ntok) acc[j] += __ldcg(theirs + (c + j) * kRows);
-          }
-          float v[32];
-          scale32(sh.sx[db] + c, sw, acc, v);
-          const int left = pl.ntok - c;
-          const int64_t tok = pl.tok0 + c;
-          if (a.mode == INT8_DOWN) {
-            float* z = static_cast<float*>(a.y) + row;
-            if (row < a.n)
+              if (j < left) y[static_cast<int64_t>(j) * a.n] = v[j];
+        } else {
+          if (a.mode == INT8_UP) {
 #pragma unroll
-              for (int j = 0; j < (NT < 32 ? NT : 32); ++j)
-                if (j < left) z[static_cast<int64_t>(sh.slot[db][c + j]) * a.n] = __fmul_rn(v[j], sh.tw[db][c + j]);
-          } else if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F32) {
-            float* y = static_cast<float*>(a.y) + tok * a.n + row;
-            if (row < a.n)
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < left) y[static_cast<int64_t>(j) * a.n] = v[j];
-          } else {
-            if (a.mode == INT8_UP) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float r = v[j] < 0.0f ? 0.0f : v[j];   // (a NaN stays)
-                v[j] = __fmul_rn(r, r);
-              }
+            for (int j = 0; j < 32; ++j) {
+              const float r = v[j] < 0.0f ? 0.0f : v[j];   // (a NaN stays)
+              v[j] = __fmul_rn(r, r);
             }
-            uint16_t* y = static_cast<uint16_t*>(a.y) + tok * a.n;
-            const bool pairs = (a.n & 1) == 0;
-            if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F16) store16<false>(y, a.n, row, a.n - row, pairs, left, v);
-            else store16<true>(y, a.n, row, a.n - row, pairs, left, v);
           }
+          uint16_t* y = static_cast<uint16_t*>(a.y) + tok * a.n;
+          const bool pairs = (a.n & 1) == 0;
+          if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F16) store16<false>(y, a.n, row, a.n - row, pairs, left, v);
+          else store16<true>(y, a.n, row, a.n - row, pairs, left, v);
         }
       }
       tc_fence_before();
       mbar_arrive(&sh.dempty[db]);
-      ++ti;
     }
   }
 

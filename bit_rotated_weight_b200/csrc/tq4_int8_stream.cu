@@ -100,7 +100,7 @@ struct Sixteen {
   }
 };
 template <typename T>
-__device__ __noinline__ uint4 codes16(Sixteen<T> x, RowUnit u) {
+__device__ __forceinline__ uint4 codes16(Sixteen<T> x, RowUnit u) {
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < Sixteen<T>::kVecs; ++i) {
@@ -110,7 +110,7 @@ __device__ __noinline__ uint4 codes16(Sixteen<T> x, RowUnit u) {
 #pragma unroll
       for (int j = 0; j < Vec<T>::N; ++j) v[j] *= u.lift;
     uint32_t b[Vec<T>::N / 4];
-    codes_of(u, v, b);
+    Vec<T>::codes(u, v, b);
 #pragma unroll
     for (int j = 0; j < Vec<T>::N / 4; ++j) c[i * (Vec<T>::N / 4) + j] = b[j];
   }
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
   uint8_t* btiles = ring + stages * kStageBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
   if (warp == 0) {
     // (a lane per barrier)
@@ -256,48 +256,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp <= kIssuers) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_i8(kRows, kTok);
-      const int me = warp - 1;
-      int ti = 0, turn3 = 0;   // whose turn the tile's first k step is
-      bool ok = true, fresh = true;   // the first tile of a segment
+    // The whole warp walks, one elected lane issues: values that are the same
+    // in every lane stay in the uniform registers that the MMA takes them from.
+    const int me = warp - 1;
+    int ti = 0, turn3 = 0;   // whose turn the tile's first k step is
+    bool ok = true, fresh = true;   // the first tile of a segment
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abortp)) != 0; };
 #pragma unroll 1
-      for (; ok && w.left > 0; w.next(), ++ti) {
-        const int si = w.seg - seg0, buf = buffers == 2 ? si & 1 : 0, turn = buffers == 2 ? si >> 1 : si, db = ti & 1;
-        if (fresh && !mbar_wait(&sh.bfull[buf], turn & 1, abortp)) break;
-        fresh = false;
-        if (!mbar_wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp)) break;
-        tc_fence_after();
-        const uint32_t d_addr = tmem + db * kAcc + me * kTok;
-        const int first = me >= turn3 ? me - turn3 : me - turn3 + kIssuers;   // its first k step of this tile
-        Place p = pos;
-        p.skip(first);
+    for (; ok && w.left > 0; w.next(), ++ti) {
+      const int si = w.seg - seg0, buf = buffers == 2 ? si & 1 : 0, turn = buffers == 2 ? si >> 1 : si, db = ti & 1;
+      if (fresh && !wait(&sh.bfull[buf], turn & 1)) break;
+      fresh = false;
+      if (!wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u)) break;
+      tc_fence_after();
+      const uint32_t d_addr = tmem + db * kAcc + me * kTok;
+      const int first = me >= turn3 ? me - turn3 : me - turn3 + kIssuers;   // its first k step of this tile
+      Place p = pos;
+      p.skip(first);
 #pragma unroll 1
-        for (int kk = first; kk < steps; kk += kIssuers) {
-          if (!mbar_wait(&sh.full[p.at], p.phase, abortp)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = sdesc_k128(smem_u32(ring + p.at * kStageBytes));
-          const uint64_t bd = sdesc_k128(smem_u32(btiles + buf * b_bytes + kk * kTileB));
-#pragma unroll
-          for (int q = 0; q < kStep / 32; ++q)
-            mma_i8(d_addr, ad + q * 2, bd + q * 2, idesc, (kk > first || q) ? 1u : 0u);   // (32 bytes on: 2 units of 16)
-          mma_commit(&sh.empty[p.at]);
-          p.skip(kIssuers);
-        }
+      for (int kk = first; kk < steps; kk += kIssuers) {
+        ok = wait(&sh.full[p.at], p.phase);
         if (!ok) break;
-        pos.skip(steps);
-        turn3 = (turn3 + steps) % kIssuers;
-        mma_commit(&sh.dfull[db]);
-        if (w.last_of_segment()) {
-          mma_commit(&sh.bempty[buf]);
-          fresh = true;
+        tc_fence_after();
+        const uint64_t ad = sdesc_k128(smem_u32(ring + p.at * kStageBytes));
+        const uint64_t bd = sdesc_k128(smem_u32(btiles + buf * b_bytes + kk * kTileB));
+        if (elect_one()) {
+#pragma unroll
+          for (int q = 0; q < kStep / 32; ++q)   // (32 bytes on: 2 units of 16)
+            mma_i8(d_addr, ad + q * 2, bd + q * 2, idesc_i8(kRows, kTok), (kk > first || q) ? 1u : 0u);
+          mma_commit(&sh.empty[p.at]);
         }
+        __syncwarp();
+        p.skip(kIssuers);
       }
-      // MMAs and the arrivals of the commits above end before the CTA does: a
-      // late arrival would meet the barriers of the CTA that comes after it
+      if (!ok) break;
+      pos.skip(steps);
+      turn3 = (turn3 + steps) % kIssuers;
+      fresh = w.last_of_segment();
+      if (elect_one()) {
+        mma_commit(&sh.dfull[db]);
+        if (fresh) mma_commit(&sh.bempty[buf]);
+      }
+      __syncwarp();
+    }
+    // MMAs and the arrivals of the commits above end before the CTA does: a
+    // late arrival would meet the barriers of the CTA that comes after it
+    if (elect_one()) {
       mma_commit(&sh.drained[me]);
       int8_drain_wait(&sh.drained[me], 0);
     }

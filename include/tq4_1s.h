@@ -389,8 +389,7 @@ int tq4_1s_int8_quantize(const void* W, int dtype, const tq4_1s_int8_weight* out
  * fp32(q * scale). */
 int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4_stream_t stream);
 
-/* Bytes of workspace tq4_1s_linear_int8 needs (the quantized activations, and
- * for medium m the parts of cut tiles); 0 on invalid arguments, m == 0, and
+/* Bytes of workspace tq4_1s_linear_int8 needs (the quantized activations); 0 on invalid arguments, m == 0, and
  * for m <= 16 with k <= 9216, which needs none (ws may then be NULL). */
 size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w);
 
