@@ -222,16 +222,20 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restri
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int j0 = 0; j0 < topk; j0 += 8) {
     float4 v[8];
-    bool ok[8];
+    int32_t e[8];
+    // (a skipped slot's row is read too, whatever it holds: a load that waits
+    // for its id would come a memory latency later)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int32_t e = j0 + j < topk ? __ldg(idt + j0 + j) : -1;
-      ok[j] = e >= 0 && e < num_experts;
-      if (ok[j]) v[j] = __ldcs(zt + static_cast<int64_t>(j0 + j) * hg);
+      e[j] = -1;
+      if (j0 + j < topk) {
+        v[j] = __ldcs(zt + static_cast<int64_t>(j0 + j) * hg);
+        e[j] = __ldg(idt + j0 + j);
+      }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (ok[j]) {
+      if (e[j] >= 0 && e[j] < num_experts) {
         s.x = __fadd_rn(s.x, v[j].x);
         s.y = __fadd_rn(s.y, v[j].y);
         s.z = __fadd_rn(s.z, v[j].z);
@@ -266,10 +270,15 @@ __global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __re
   for (int e = tid; e < num_experts; e += 1024) count[e] = 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  for (int64_t p = tid; p < slots; p += 1024) {
-    const int32_t e = ids[p];
-    if (e >= 0 && e < num_experts) atomicAdd(&count[e], 1);
-    else s_bad = 1;
+  for (int64_t p0 = tid; p0 < slots; p0 += 8 * 1024) {   // (eight loads in flight a thread)
+    int32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = p0 + j * 1024 < slots ? __ldg(ids + p0 + j * 1024) : INT32_MIN;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (e[j] >= 0 && e[j] < num_experts) atomicAdd(&count[e[j]], 1);
+      else if (p0 + j * 1024 < slots) s_bad = 1;
+    }
   }
   __syncthreads();
   int32_t rows0 = 0, segs0 = 0;   // of the experts before this pass
