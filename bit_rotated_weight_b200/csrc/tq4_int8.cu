@@ -421,8 +421,17 @@ Plan plan_dense(int64_t m, int64_t n, int64_t k, int sms) {
   p.row_tiles = (n + 127) / 128;
   p.tok_tiles = (m + p.nt - 1) / p.nt;
   p.ksteps = (k + 127) / 128;
-  const int64_t tiles = p.row_tiles * p.tok_tiles;
+  int64_t tiles = p.row_tiles * p.tok_tiles;
   p.grid = static_cast<int>(tiles < sms ? tiles : sms);
+  // Many tiles: two CTAs share one of 256 rows x 256 tokens (8192 x 14336 x
+  // 4096: 353 us sustained, 400 without; in one wave the launch costs more
+  // than the copies saved: 1024 x 4096 x 4096 22.4 and 20.5).
+  if (p.nt == 256 && (n + 255) / 256 * p.tok_tiles > sms / 2) {
+    p.nt = kInt8Pair;
+    p.row_tiles = (n + 255) / 256;
+    tiles = p.row_tiles * p.tok_tiles;
+    p.grid = 2 * static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+  }
   return p;
 }
 
@@ -578,7 +587,7 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
-  if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) || !encode_i8_map(&tx, xq, 0, m, w->k, p.nt))
+  if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) || !encode_i8_map(&tx, xq, 0, m, w->k, p.nt == kInt8Pair ? 128 : p.nt))
     return TQ_ERR_CUDA;
   RowsArgs r{};
   r.x = x;
@@ -642,11 +651,15 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
 
   // few rows an expert: the products quantize their rows themselves
   const bool stream_rows = L.nt == kStreamTokens && int8_stream_fits(H) && int8_stream_fits(I);
-  int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(
-      topk_ids, L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
-      stream_rows ? i32(L.pairs) : nullptr, f32(L.row_w));
-  note_launches(1);
-  if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  // and where the slots fit a block's routing they need no kernel for that
+  const bool routed = stream_rows && L.slots <= kStreamSlots;
+  if (!routed) {
+    int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(
+        topk_ids, L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
+        stream_rows ? i32(L.pairs) : nullptr, f32(L.row_w));
+    note_launches(1);
+    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
+  }
   const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
   if (stream_rows) {
     Int8StreamArgs s{};
@@ -659,10 +672,17 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
     s.topk = topk;
     s.ldx = H;
     s.x = x;
-    s.segs = segs;
-    s.nseg = i32(L.nseg);
-    s.pairs = i32(L.pairs);
-    s.row_w = f32(L.row_w);
+    if (routed) {
+      s.ids = topk_ids;
+      s.topk_w = topk_w;
+      s.slots = static_cast<int32_t>(L.slots);
+      s.experts = static_cast<int32_t>(E);
+    } else {
+      s.segs = segs;
+      s.nseg = i32(L.nseg);
+      s.pairs = i32(L.pairs);
+      s.row_w = f32(L.row_w);
+    }
     s.wscale = up->wscale;
     s.y = base + L.h;
     if (launch_int8_stream(dtype, tu, s, tiles_up, sms, st) != cudaSuccess) return TQ_ERR_CUDA;

@@ -28,7 +28,10 @@ struct Int8GemmArgs {
 bool encode_i8_map(CUtensorMap* m, const int8_t* base, int64_t experts, int64_t rows, int64_t k, int box_rows);
 
 
-// nt: 16, 32, 64, 128 or 256 tokens a tile (the box rows of tx).
+// nt: 16, 32, 64, 128 or 256 tokens a tile (the box rows of tx), or kInt8Pair:
+// dense tiles of 256 weight rows (row_tiles counts those) x 256 tokens shared
+// by two CTAs (an even grid), whose tx has 128 box rows.
+constexpr int kInt8Pair = 512;
 cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int nt, int grid,
                              cudaStream_t st);
 
@@ -47,9 +50,13 @@ struct Int8StreamArgs {
   const int32_t* nseg;
   const int32_t* pairs;
   const float* row_w;
+  const int32_t* ids;       // grouped without segs: the kernel routes [slots] ids itself,
+  const float* topk_w;      // with their weights
+  int32_t slots, experts;   // (slots <= kStreamSlots)
   const float* wscale;
   void* y;                  // as Int8GemmArgs
 };
+constexpr int kStreamSlots = 128;
 // Whether rows of k elements fit (their codes stay in shared memory).
 bool int8_stream_fits(int64_t k);
 // The cluster size for a dense product of row_tiles x ksteps.

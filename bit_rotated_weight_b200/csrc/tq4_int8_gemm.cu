@@ -120,6 +120,57 @@ __device__ __forceinline__ void store16(uint16_t* y, int64_t n, int row, int row
   }
 }
 
+// A thread's share of a tile: one weight row, tokens [col0, col0 + cols).
+template <int NT>
+__device__ __forceinline__ void finish_columns(const Int8GemmArgs& a, const Place& pl, int row, float sw,
+                                               uint32_t d_addr, int col0, int cols, const float* sx, const float* tw,
+                                               const int32_t* slot) {
+#pragma unroll 1
+  for (int c = col0; c < min(pl.ntok, col0 + cols); c += 32) {
+    int32_t acc[32];
+    {
+      uint32_t r0[16], r1[16];
+      tmem_ld16(d_addr + c, r0);
+      if (NT > 16) tmem_ld16(d_addr + c + 16, r1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        acc[j] = static_cast<int32_t>(r0[j]);
+        acc[16 + j] = NT > 16 ? static_cast<int32_t>(r1[j]) : 0;
+      }
+    }
+    float v[32];
+    scale32(sx + c, sw, acc, v);
+    const int left = pl.ntok - c;
+    const int64_t tok = pl.tok0 + c;
+    if (a.mode == INT8_DOWN) {
+      float* z = static_cast<float*>(a.y) + row;
+      if (row < a.n)
+#pragma unroll
+        for (int j = 0; j < (NT < 32 ? NT : 32); ++j)
+          if (j < left) z[static_cast<int64_t>(slot[c + j]) * a.n] = __fmul_rn(v[j], tw[c + j]);
+    } else if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F32) {
+      float* y = static_cast<float*>(a.y) + tok * a.n + row;
+      if (row < a.n)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j < left) y[static_cast<int64_t>(j) * a.n] = v[j];
+    } else {
+      if (a.mode == INT8_UP) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float r = v[j] < 0.0f ? 0.0f : v[j];   // (a NaN stays)
+          v[j] = __fmul_rn(r, r);
+        }
+      }
+      uint16_t* y = static_cast<uint16_t*>(a.y) + tok * a.n;
+      const bool pairs = (a.n & 1) == 0;
+      if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F16) store16<false>(y, a.n, row, a.n - row, pairs, left, v);
+      else store16<true>(y, a.n, row, a.n - row, pairs, left, v);
+    }
+  }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -272,50 +323,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       const int row = pl.row0 + t;
       const uint32_t d_addr = tmem + lane_base + db * NT;
       const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
-#pragma unroll 1
-      for (int c = col0; c < min(pl.ntok, col0 + kCols); c += 32) {
-        int32_t acc[32];
-        {
-          uint32_t r0[16], r1[16];
-          tmem_ld16(d_addr + c, r0);
-          if (NT > 16) tmem_ld16(d_addr + c + 16, r1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            acc[j] = static_cast<int32_t>(r0[j]);
-            acc[16 + j] = NT > 16 ? static_cast<int32_t>(r1[j]) : 0;
-          }
-        }
-        float v[32];
-        scale32(sh.sx[db] + c, sw, acc, v);
-        const int left = pl.ntok - c;
-        const int64_t tok = pl.tok0 + c;
-        if (a.mode == INT8_DOWN) {
-          float* z = static_cast<float*>(a.y) + row;
-          if (row < a.n)
-#pragma unroll
-            for (int j = 0; j < (NT < 32 ? NT : 32); ++j)
-              if (j < left) z[static_cast<int64_t>(sh.slot[db][c + j]) * a.n] = __fmul_rn(v[j], sh.tw[db][c + j]);
-        } else if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F32) {
-          float* y = static_cast<float*>(a.y) + tok * a.n + row;
-          if (row < a.n)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < left) y[static_cast<int64_t>(j) * a.n] = v[j];
-        } else {
-          if (a.mode == INT8_UP) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float r = v[j] < 0.0f ? 0.0f : v[j];   // (a NaN stays)
-              v[j] = __fmul_rn(r, r);
-            }
-          }
-          uint16_t* y = static_cast<uint16_t*>(a.y) + tok * a.n;
-          const bool pairs = (a.n & 1) == 0;
-          if (a.mode == INT8_DENSE && a.dtype == TQ_DTYPE_F16) store16<false>(y, a.n, row, a.n - row, pairs, left, v);
-          else store16<true>(y, a.n, row, a.n - row, pairs, left, v);
-        }
-      }
+      finish_columns<NT>(a, pl, row, sw, d_addr, col0, kCols, sh.sx[db], sh.tw[db], sh.slot[db]);
       tc_fence_before();
       mbar_arrive(&sh.dempty[db]);
     }
@@ -325,6 +333,224 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// ------------------------------------------------------------------ pairs
+// The product of many tokens: two CTAs (a cluster) share a tile of 256 weight
+// rows x 256 tokens.  Each copies its own 128 rows of W and half of the
+// tokens, 32 KB a k step instead of 48 KB for half a tile, and the MMAs of
+// cta_group::2, issued by the first CTA, read both halves; each CTA finishes
+// its own 128 rows.  The first CTA's `full` barriers count the bytes of both,
+// its commits free the stages of both, and its `dempty` counts the epilogue
+// warps of both.
+constexpr int kPairTok = 256;
+constexpr int kPairStageBytes = kABytes + kPairTok / 2 * kStep;
+constexpr int kPairStages = (200 * 1024) / kPairStageBytes;
+constexpr int kPairThreads = 384, kPairEpilogue = 256;
+constexpr size_t kPairSmem = static_cast<size_t>(kPairStages) * kPairStageBytes + 1024;
+
+struct PairShared {
+  uint64_t full[kPairStages];
+  uint64_t empty[kPairStages];
+  uint64_t dfull[2];
+  uint64_t dempty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int epi_ok[2];
+  alignas(16) float sx[2][kPairTok];
+};
+
+// Rows of the pair's tile: the tokens are cut in two halves of `half`.
+__device__ __forceinline__ Place place_of_pair(const Int8GemmArgs& a, int32_t tile, int rank, int& half) {
+  Place p;
+  const int32_t r = tile / a.tok_tiles;
+  p.expert = 0;
+  p.row0 = r * (2 * kRows) + rank * kRows;
+  p.tok0 = (tile - r * a.tok_tiles) * kPairTok;
+  p.ntok = min(kPairTok, a.m - p.tok0);
+  half = (p.ntok + 31) / 32 * 16;
+  return p;
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ Int8GemmArgs a) {
+  __shared__ PairShared sh;
+  extern __shared__ uint8_t dyn_smem[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.dfull[i], 1);
+      mbar_init(&sh.dempty[i], 2 * kPairEpilogue / 32);
+    }
+    mbar_init(&sh.mma_done, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 2) {
+    tmem_alloc2(&sh.tmem_base, 512);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();   // both CTAs' barriers are there
+  cluster_wait();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abortp = &sh.abort_flag;
+  const int tiles = a.row_tiles * a.tok_tiles, tile0 = blockIdx.x / 2, stride = gridDim.x / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int early = 0;   // stages whose weight half is already on its way
+      for (int tile = tile0; tile < tiles && early < kPairStages; tile += stride) {
+        int half;
+        const Place pl = place_of_pair(a, tile, rank, half);
+        for (int kk = 0; kk < a.ksteps && early < kPairStages; ++kk, ++early) {
+          if (rank == 0) mbar_arrive_expect_tx(&sh.full[early], 2 * kPairStageBytes);
+          tma_load_3d_pair(smem + early * kPairStageBytes, &tm_w, in_cta(&sh.full[early], 0), kk * kStep, pl.row0, 0);
+        }
+      }
+      pdl_wait();
+      int li = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < tiles; tile += stride) {
+        int half;
+        const Place pl = place_of_pair(a, tile, rank, half);
+        for (int kk = 0; kk < a.ksteps; ++kk, ++li) {
+          uint8_t* st = smem + s * kPairStageBytes;
+          const uint32_t bar = in_cta(&sh.full[s], 0);
+          if (li >= early) {
+            if (!mbar_wait(&sh.empty[s], ph ^ 1u, abortp)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kPairStageBytes);
+            tma_load_3d_pair(st, &tm_w, bar, kk * kStep, pl.row0, 0);
+          }
+          tma_load_2d_pair(st + kABytes, &tm_x, bar, kk * kStep, pl.tok0 + rank * half);
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (*abortp && rank == 0)   // let the copies in flight land (both CTAs stay until the barrier at the end)
+        for (int i = 0; i < min(li, kPairStages); ++i) {
+          s = s == 0 ? kPairStages - 1 : s - 1;
+          if (s == kPairStages - 1) ph ^= 1u;
+          int8_drain_wait(&sh.full[s], ph);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int s = 0, ti = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = tile0; ok && tile < tiles; tile += stride, ++ti) {
+        const int db = ti & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u, abortp))) break;
+        tc_fence_after();
+        int half;
+        place_of_pair(a, tile, rank, half);
+        const uint32_t d_addr = tmem + db * kPairTok, idesc = idesc_i8(2 * kRows, 2 * half);
+        for (int kk = 0; kk < a.ksteps; ++kk) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&sh.full[s], ph, abortp));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t ad = sdesc_k128(smem_u32(smem + s * kPairStageBytes));
+          const uint64_t bd = sdesc_k128(smem_u32(smem + s * kPairStageBytes + kABytes));
+          if (elect_one()) {
+#pragma unroll
+            for (int q = 0; q < kStep / 32; ++q)   // (32 bytes on: 2 units of 16)
+              mma_i8_pair(d_addr, ad + q * 2, bd + q * 2, idesc, (kk | q) ? 1u : 0u);
+            mma_commit_pair(&sh.empty[s]);
+          }
+          __syncwarp();
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (ok && elect_one()) mma_commit_pair(&sh.dfull[db]);
+        __syncwarp();
+      }
+      if (elect_one()) {
+        mma_commit_pair(&sh.mma_done);
+        int8_drain_wait(&sh.mma_done, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    pdl_wait();   // the scales come from the kernel before
+    const int t = (warp & 3) * 32 + lane;
+    const int col0 = ((warp - 4) >> 2) * (kPairTok / 2);   // two warps share 32 rows, half of the tokens each
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int ti = 0;
+    for (int tile = tile0; tile < tiles; tile += stride, ++ti) {
+      const int db = ti & 1;
+      int half;
+      const Place pl = place_of_pair(a, tile, rank, half);
+      {
+        const int j = threadIdx.x - 128;   // (the buffer of the last tile but one: every thread has left it)
+        sh.sx[db][j] = j < pl.ntok ? __ldcg(a.xscale + pl.tok0 + j) : 0.0f;
+      }
+      if (threadIdx.x == 128) sh.epi_ok[db] = mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp) ? 1 : 0;
+      named_bar_sync(1, kPairEpilogue);
+      if (!sh.epi_ok[db]) break;
+      tc_fence_after();
+      const int row = pl.row0 + t;
+      const float sw = row < a.n ? __ldg(a.wscale + row) : 0.0f;
+      finish_columns<kPairTok>(a, pl, row, sw, tmem + lane_base + db * kPairTok, col0, kPairTok / 2, sh.sx[db],
+                               nullptr, nullptr);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(in_cta(&sh.dempty[db], 0));
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();   // neither CTA leaves, or frees its tensor memory, while the other may still reach it
+  cluster_wait();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc2(tmem, 512);
+}
+
+cudaError_t launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kPairSmem));
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, int8_pair_kernel, tw, tx, a);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaGetLastError();
 }
 
 template <int NT>
@@ -356,6 +582,7 @@ cudaError_t launch(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmA
 cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int nt, int grid,
                              cudaStream_t st) {
   switch (nt) {
+    case kInt8Pair: return launch_pair(tw, tx, a, grid, st);
     case 16: return launch<16>(tw, tx, a, grid, st);
     case 32: return launch<32>(tw, tx, a, grid, st);
     case 64: return launch<64>(tw, tx, a, grid, st);

@@ -21,9 +21,12 @@
 // tile, each with a range of k.  They exchange the rows' largest values and
 // their int32 sums by asynchronous stores into each other's shared memory that
 // the receiver counts in bytes: no workspace, no second kernel.
-// The code is kept small (no inlined copies of the rounding, no unrolled role
-// loops): a call of a few microseconds runs most of it once, and fetching
-// instructions was most of its time.
+// Grouped, with at most 128 slots, every CTA sorts the slots by expert itself
+// (a count of smaller ids per slot): a kernel for that took 3 us of a token's
+// 24, and its results came three memory latencies later.  The down projection
+// does so, and starts its weight copies, before it waits for the up projection.
+// Role loops are not unrolled: a call of a few microseconds runs most of the
+// code once, and fetching instructions was most of its time.
 // Every wait on an mbarrier is bounded.
 #include "tq4_int8_mma.cuh"
 #include "tq4_int8_rows.cuh"
@@ -56,14 +59,58 @@ struct Shared {
   float sx[2][kTok], tw[2][kTok];
   int32_t slot[2][kTok];
   alignas(16) int32_t part[kRows * kPartRow];   // cluster form: [CTA][its rows][token]
+  // routing in the kernel
+  int32_t nseg;
+  alignas(16) int32_t id[kStreamSlots];
+  int32_t sub[kStreamSlots];               // segments of a slot's expert, at its first slot
+  int4 segs[kStreamSlots];
+  int32_t pairs[kStreamSlots];
+  float row_w[kStreamSlots];
 };
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ uint32_t at_rank(uint32_t local, uint32_t rank) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  return remote;
+// Sorts the slots by expert, by the whole block: a slot's row is the number of
+// slots with a smaller id, or the same id earlier.  Ids out of range are left
+// out.  (The ids are ready before this call's first kernel.)
+__device__ __forceinline__ void route(Shared& sh, const Int8StreamArgs& a) {
+  const int t = threadIdx.x;
+  if (t == 0) sh.nseg = 0;
+  int32_t id = INT32_MAX;
+  float w = 0.0f;
+  if (t < kStreamSlots) {
+    if (t < a.slots) {
+      id = __ldcg(a.ids + t);
+      w = __ldcg(a.topk_w + t);
+      if (id < 0 || id >= a.experts) {
+        if (blockIdx.x == 0) raise_status(TQ_DEV_BAD_ROUTING);
+        id = INT32_MAX;
+      }
+    }
+    sh.id[t] = id;
+    sh.sub[t] = 0;
+  }
+  __syncthreads();
+  int less = 0, same = 0, before = 0;
+  if (id != INT32_MAX) {
+#pragma unroll 1
+    for (int q = 0; q < a.slots; q += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(&sh.id[q]);
+      less += (o.x < id) + (o.y < id) + (o.z < id) + (o.w < id);
+      same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+      before += (o.x == id && q < t) + (o.y == id && q + 1 < t) + (o.z == id && q + 2 < t) + (o.w == id && q + 3 < t);
+    }
+    sh.pairs[less + before] = t;
+    sh.row_w[less + before] = w;
+    if (before == 0) sh.sub[t] = (same + kTok - 1) / kTok;
+  }
+  __syncthreads();
+  if (id != INT32_MAX && before == 0) {
+    int at = 0;
+#pragma unroll 1
+    for (int q = 0; q < a.slots; ++q) at += sh.id[q] < id ? sh.sub[q] : 0;
+    for (int i = 0; i < same; i += kTok) sh.segs[at++] = make_int4(id, less + i, min(kTok, same - i), 0);
+    atomicAdd(&sh.nseg, (same + kTok - 1) / kTok);
+  }
+  __syncthreads();
 }
 
 // Quantizer threads of a row, for a tile of `tokens` rows.
@@ -182,23 +229,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) sh.top[lane >> 4][lane & 15] = 0;
-  if (CLUSTER) {
-    __syncthreads();
-    cluster_arrive();   // every CTA's barriers are there
-  }
-  // Tensor memory is taken after the wait for the kernel before, and the next
-  // one let in after that: of two that wait for one another, neither may hold
-  // columns that the other still has to take.
-  pdl_wait();
-  if (warp == 2) {
-    tmem_alloc(&sh.tmem_base, 2 * kAcc);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  pdl_launch_dependents();
-  const uint32_t tmem = sh.tmem_base;
+  if (CLUSTER) cluster_arrive();   // every CTA's barriers are there
+  // What a role reads before its wait for the kernel before is this call's
+  // input.  Tensor memory is taken after the wait, and the next kernel let in
+  // after that: of two that wait for one another, neither may hold columns
+  // that the other still has to take.
+  const bool routed = !CLUSTER && a.ids != nullptr, ahead = routed && a.mode == INT8_DOWN;
+  if (!ahead) pdl_wait();
+  if (routed) route(sh, a);
+  if (ahead && warp != 0) pdl_wait();
+  if (warp >= 1 && warp < 8) {
+    if (warp == 2) {
+      tmem_alloc(&sh.tmem_base, 2 * kAcc);
+      tmem_relinquish();
+      tc_fence_before();
+    }
+    named_bar_sync(3, 7 * 32);
+    tc_fence_after();
+    if (threadIdx.x == 64) pdl_launch_dependents();
+  }
   volatile int* abortp = &sh.abort_flag;
   Tiles w;
   int k0 = 0, k1 = a.ksteps, b_bytes = a.ksteps * kTileB;
@@ -211,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     k1 = a.ksteps * (rank + 1) / a.parts;
     b_bytes = (a.ksteps + a.parts - 1) / a.parts * kTileB;
   } else {
-    const int32_t tiles = a.segs ? __ldcg(a.nseg) * a.row_tiles : a.row_tiles;
+    const int32_t segs = routed ? sh.nseg : a.segs ? __ldcg(a.nseg) : 1;
+    const int32_t tiles = segs * a.row_tiles;
     const int32_t per = tiles / static_cast<int>(gridDim.x), rest = tiles - per * static_cast<int>(gridDim.x);
     const int32_t c = blockIdx.x, first = c * per + min(c, rest);
     w.left = per + (c < rest ? 1 : 0);
@@ -220,7 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int32_t seg0 = w.seg;
   const int steps = k1 - k0;
-  auto segment = [&](int32_t s) { return a.segs ? __ldcg(a.segs + s) : make_int4(0, 0, a.m, 0); };
+  auto segment = [&](int32_t s) {
+    return routed ? sh.segs[s] : a.segs ? __ldcg(a.segs + s) : make_int4(0, 0, a.m, 0);
+  };
+  auto slot_of = [&](int32_t row) { return routed ? sh.pairs[row] : __ldcg(a.pairs + row); };
   Place pos{stages, 0, 0};
 
   if (warp == 0) {
@@ -269,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fresh = false;
       if (!wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u)) break;
       tc_fence_after();
-      const uint32_t d_addr = tmem + db * kAcc + me * kTok;
+      const uint32_t d_addr = sh.tmem_base + db * kAcc + me * kTok;
       const int first = me >= turn3 ? me - turn3 : me - turn3 + kIssuers;   // its first k step of this tile
       Place p = pos;
       p.skip(first);
@@ -319,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = q / tpr, i0 = q - r * tpr;
       const bool live = r < sg.z;
       const int row = sg.y + r;
-      const int64_t from = !live ? 0 : a.mode == INT8_UP ? __ldcg(a.pairs + row) / a.topk : row;
+      const int64_t from = !live ? 0 : a.mode == INT8_UP ? slot_of(row) / a.topk : row;
       const T* x = static_cast<const T*>(a.x) + from * a.ldx;
       const int c0 = k0 * (kStep / 16), c1 = live ? min(k1 * (kStep / 16), a.k / 16) : 0;   // chunks of 16
       Sixteen<T> hold[kHold];
@@ -352,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader)
           for (int p = 0; p < a.parts; ++p)
             asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
-                             at_rank(smem_u32(&sh.tops[rank][at]), p)),
-                         "r"(top), "r"(at_rank(smem_u32(&sh.maxima), p))
+                             in_cta(&sh.tops[rank][at], p)),
+                         "r"(top), "r"(in_cta(&sh.maxima, p))
                          : "memory");
         if (!mbar_wait(&sh.maxima, 0, abortp)) ok = false;
         if (live) {
@@ -372,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!u.finite) raise_status(TQ_DEV_NONFINITE);
         sh.sx[buf][r] = u.scale;
         if (a.mode == INT8_DOWN) {
-          sh.slot[buf][r] = __ldcg(a.pairs + row);
-          sh.tw[buf][r] = __ldcg(a.row_w + row);
+          sh.slot[buf][r] = slot_of(row);
+          sh.tw[buf][r] = routed ? sh.row_w[row] : __ldcg(a.row_w + row);
         }
       }
       // (rows and columns without a value keep what was there: it meets
@@ -428,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < accs; ++i) {
           uint32_t d[kTok];
-          tmem_ld16(tmem + lane_base + db * kAcc + (turn3 + i) % kIssuers * kTok, d);
+          tmem_ld16(sh.tmem_base + lane_base + db * kAcc + (turn3 + i) % kIssuers * kTok, d);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < kTok; ++j) acc[j] += static_cast<int32_t>(d[j]);
@@ -439,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // counted by its owner, so it is sent after a timeout too
         cluster_wait();
         const int per = kRows / a.parts, owner = t / per;
-        const uint32_t to = at_rank(smem_u32(&sh.part[(rank * per + (t - owner * per)) * kPartRow]), owner);
-        const uint32_t bar = at_rank(smem_u32(&sh.sums), owner);
+        const uint32_t to = in_cta(&sh.part[(rank * per + (t - owner * per)) * kPartRow], owner);
+        const uint32_t bar = in_cta(&sh.sums, owner);
 #pragma unroll
         for (int j = 0; j < kTok; j += 4)
           if (j < sg.z)
@@ -497,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, 2 * kAcc);
+  if (warp == 2) tmem_dealloc(sh.tmem_base, 2 * kAcc);
 }
 
 template <typename T>
@@ -513,7 +567,7 @@ cudaError_t launch_as(const CUtensorMap& tw, const Int8StreamArgs& a, int64_t mo
   if (e != cudaSuccess) return e;
   const int part_steps = (a.ksteps + a.parts - 1) / a.parts, b_bytes = part_steps * kTileB;
   int buffers = 1;
-  if (a.segs && kSpace - 2 * b_bytes >= 4 * kStageBytes) buffers = 2;
+  if ((a.segs || a.ids) && kSpace - 2 * b_bytes >= 4 * kStageBytes) buffers = 2;
   int stages = (kSpace - buffers * b_bytes) / kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (a.parts > 1 && stages >= part_steps) stages = part_steps;   // (none is used again)

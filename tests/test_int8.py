@@ -174,6 +174,18 @@ def test_linear_matches_plain(m, n, k, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,dtype", [
+    (2304, 4096, 32, BF16), (2309, 4097, 160, BF16), (2500, 4099, 96, F32), (2400, 4360, 416, F16),
+    (5000, 2561, 64, BF16), (9000, 1100, 1024, BF16),
+])
+def test_linear_many_tokens(m, n, k, dtype):
+    # tiles shared by two blocks: ragged ends of tokens, rows and k
+    w, q, s = weight(n, k, n + k)
+    check_linear(torch.randn(m, k, generator=gen(m + k)).to(dtype), w, q, s)
+    assert tq.tq4_1s_get_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 40])
 def test_linear_largest_sums(m):
     # every product 127 * 127 at the largest k: the int32 sums reach 2.11e9
