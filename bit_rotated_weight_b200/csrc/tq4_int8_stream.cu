@@ -16,7 +16,10 @@
 //   warps 8-15  quantize the tokens into the MMAs' B tiles (128-byte swizzle):
 //               rows' largest values, then codes, 16 of them a thread a turn.
 // Persistent form: a CTA takes a contiguous range of (segment, row tile), so
-// that a segment's tokens are quantized about once per CTA (two buffers).
+// that a segment's tokens are quantized about once per CTA.  (Their codes have
+// one buffer: a second one took the room of three weight stages, and an SM's
+// rate is its stages over the 2 us from a stage's copy to its release; 1 token
+// of 6 x 128 experts 20.1 us, 21.3 with two.)
 // Cluster form, for a dense product of few row tiles: `parts` CTAs share a row
 // tile, each with a range of k.  They exchange the rows' largest values and
 // their int32 sums by asynchronous stores into each other's shared memory that
@@ -41,7 +44,7 @@ constexpr int kThreads = 512, kQuantThreads = 256, kEpilogue = 128;
 constexpr int kIssuers = 3;
 constexpr int kAcc = 64;                   // tensor-memory columns between the two sets of accumulators
 constexpr int kMaxStages = 12;
-constexpr int kSpace = 208 * 1024;         // B buffers and weight stages
+constexpr int kSpace = 208 * 1024;         // the tokens' codes and the weight stages
 constexpr int kHold = 4;                   // turns whose values a quantizer thread keeps between its two passes
 constexpr int kPartRow = 20;               // ints of a row's partial sums (16 and padding: 16-byte reads without conflicts)
 constexpr int kMaxParts = 8;
@@ -49,15 +52,15 @@ constexpr int kMaxParts = 8;
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t dfull[2], dempty[2];
-  uint64_t bfull[2], bempty[2];
+  uint64_t bfull, bempty;
   uint64_t drained[kIssuers];
   uint64_t maxima, sums;                   // cluster form: what the other CTAs send has arrived
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t top[2][kTok];                   // largest |x| of each token, as bits (persistent form)
+  uint32_t top[kTok];                      // largest |x| of each token, as bits (persistent form)
   uint32_t tops[kMaxParts][kTok];          // [CTA][row, or warp of a row] (cluster form)
-  float sx[2][kTok], tw[2][kTok];
-  int32_t slot[2][kTok];
+  float sx[kTok], tw[kTok];
+  int32_t slot[kTok];
   alignas(16) int32_t part[kRows * kPartRow];   // cluster form: [CTA][its rows][token]
   // routing in the kernel
   int32_t nseg;
@@ -198,7 +201,7 @@ struct Place {
 template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_stream_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ Int8StreamArgs a,
-                       int32_t stages, int32_t buffers) {
+                       int32_t stages) {
   __shared__ Shared sh;
   extern __shared__ uint8_t dyn_smem[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~uintptr_t(1023));
@@ -213,9 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane >= 16 && lane < 18) {
       mbar_init(&sh.dfull[lane - 16], kIssuers);
       mbar_init(&sh.dempty[lane - 16], kEpilogue);
-      mbar_init(&sh.bfull[lane - 16], kQuantThreads);
-      mbar_init(&sh.bempty[lane - 16], kIssuers + kEpilogue);   // (the epilogue reads the scales)
     } else if (lane == 18) {
+      mbar_init(&sh.bfull, kQuantThreads);
+      mbar_init(&sh.bempty, kIssuers + kEpilogue);   // (the epilogue reads the scales)
       sh.abort_flag = 0;
       for (int i = 0; i < kIssuers; ++i) mbar_init(&sh.drained[i], 1);
       if (CLUSTER) {
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     fence_mbar_init();
   }
-  if (warp == 1) sh.top[lane >> 4][lane & 15] = 0;
+  if (warp == 1 && lane < kTok) sh.top[lane] = 0;
   __syncthreads();
   if (CLUSTER) cluster_arrive();   // every CTA's barriers are there
   // What a role reads before its wait for the kernel before is this call's
@@ -251,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   volatile int* abortp = &sh.abort_flag;
   Tiles w;
-  int k0 = 0, k1 = a.ksteps, b_bytes = a.ksteps * kTileB;
+  int k0 = 0, k1 = a.ksteps;
   w.row_tiles = a.row_tiles;
   if (CLUSTER) {
     w.left = 1;
@@ -259,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.row_tile = blockIdx.x / a.parts;
     k0 = a.ksteps * rank / a.parts;
     k1 = a.ksteps * (rank + 1) / a.parts;
-    b_bytes = (a.ksteps + a.parts - 1) / a.parts * kTileB;
   } else {
     const int32_t segs = routed ? sh.nseg : a.segs ? __ldcg(a.nseg) : 1;
     const int32_t tiles = segs * a.row_tiles;
@@ -318,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abortp)) != 0; };
 #pragma unroll 1
     for (; ok && w.left > 0; w.next(), ++ti) {
-      const int si = w.seg - seg0, buf = buffers == 2 ? si & 1 : 0, turn = buffers == 2 ? si >> 1 : si, db = ti & 1;
-      if (fresh && !wait(&sh.bfull[buf], turn & 1)) break;
+      const int turn = w.seg - seg0, db = ti & 1;
+      if (fresh && !wait(&sh.bfull, turn & 1)) break;
       fresh = false;
       if (!wait(&sh.dempty[db], ((ti >> 1) & 1) ^ 1u)) break;
       tc_fence_after();
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint64_t ad = sdesc_k128(smem_u32(ring + p.at * kStageBytes));
-        const uint64_t bd = sdesc_k128(smem_u32(btiles + buf * b_bytes + kk * kTileB));
+        const uint64_t bd = sdesc_k128(smem_u32(btiles + kk * kTileB));
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < kStep / 32; ++q)   // (32 bytes on: 2 units of 16)
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fresh = w.last_of_segment();
       if (elect_one()) {
         mma_commit(&sh.dfull[db]);
-        if (fresh) mma_commit(&sh.bempty[buf]);
+        if (fresh) mma_commit(&sh.bempty);
       }
       __syncwarp();
     }
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int32_t s = seg0, n = (w.row_tile + w.left + a.row_tiles - 1) / a.row_tiles; n > 0 && w.left > 0; ++s, --n) {
-      const int si = s - seg0, buf = buffers == 2 ? si & 1 : 0, turn = buffers == 2 ? si >> 1 : si;
+      const int turn = s - seg0;
       const int4 sg = segment(s);
       const int tpr = threads_per_row(sg.z);
       const int r = q / tpr, i0 = q - r * tpr;
@@ -383,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = c0 + i0 + j * tpr;
         if (c < c1) hold[j].load(x + static_cast<int64_t>(c) * 16, wide);
       }
-      if (ok) ok = mbar_wait(&sh.bempty[buf], (turn & 1) ^ 1u, abortp);
+      if (ok) ok = mbar_wait(&sh.bempty, (turn & 1) ^ 1u, abortp);
 #pragma unroll
       for (int j = 0; j < kHold; ++j)
         if (c0 + i0 + j * tpr < c1) top = max(top, hold[j].top());
@@ -417,22 +419,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               row_top = max(row_top, *reinterpret_cast<volatile uint32_t*>(&sh.tops[p][at0 + i]));
         }
       } else {
-        if (leader) atomicMax(&sh.top[buf][r], top);
+        if (leader) atomicMax(&sh.top[r], top);
         named_bar_sync(2, kQuantThreads);
-        if (live) row_top = *reinterpret_cast<volatile uint32_t*>(&sh.top[buf][r]);
+        if (live) row_top = *reinterpret_cast<volatile uint32_t*>(&sh.top[r]);
       }
       const RowUnit u(Vec<T>::top_f32(row_top));
       if (i0 == 0 && live) {
         if (!u.finite) raise_status(TQ_DEV_NONFINITE);
-        sh.sx[buf][r] = u.scale;
+        sh.sx[r] = u.scale;
         if (a.mode == INT8_DOWN) {
-          sh.slot[buf][r] = slot_of(row);
-          sh.tw[buf][r] = routed ? sh.row_w[row] : __ldcg(a.row_w + row);
+          sh.slot[r] = slot_of(row);
+          sh.tw[r] = routed ? sh.row_w[row] : __ldcg(a.row_w + row);
         }
       }
       // (rows and columns without a value keep what was there: it meets
       // outputs that are not stored, and weights that the copy filled with 0)
-      uint8_t* b = btiles + buf * b_bytes + (r & 15) * kStep;
+      uint8_t* b = btiles + (r & 15) * kStep;
       auto put = [&](int c, const Sixteen<T>& v) {
         const int at = c - c0;   // k step and 16-byte piece of the tile, swizzled
         *reinterpret_cast<uint4*>(b + (at >> 3) * kTileB + (((at & 7) ^ (r & 7)) << 4)) = codes16<T>(v, u);
@@ -449,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       if (!CLUSTER) {
         named_bar_sync(2, kQuantThreads);   // every thread has read its row's maximum
-        if (q < kTok) sh.top[buf][q] = 0;
+        if (q < kTok) sh.top[q] = 0;
       }
-      mbar_arrive(&sh.bfull[buf]);
+      mbar_arrive(&sh.bfull);
     }
   } else {
     // ---- epilogue
@@ -463,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int4 sg = make_int4(0, 0, 0, 0);
 #pragma unroll 1
     for (; w.left > 0; w.next(), ++ti) {
-      const int si = w.seg - seg0, buf = buffers == 2 ? si & 1 : 0, turn = buffers == 2 ? si >> 1 : si, db = ti & 1;
+      const int turn = w.seg - seg0, db = ti & 1;
       if (fresh) {
         sg = segment(w.seg);
-        ok = ok && mbar_wait(&sh.bfull[buf], turn & 1, abortp);   // the scales
+        ok = ok && mbar_wait(&sh.bfull, turn & 1, abortp);   // the scales
         fresh = false;
       }
       const int row = w.row_tile * kRows + t;
@@ -520,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 4; ++j)
             if (j0 + j < sg.z)
               put_out(a.y, a.dtype, static_cast<int64_t>(j0 + j) * a.n + out_row,
-                      __fmul_rn(__fmul_rn(static_cast<float>(v[j]), sh.sx[0][j0 + j]), osw));
+                      __fmul_rn(__fmul_rn(static_cast<float>(v[j]), sh.sx[j0 + j]), osw));
         }
       } else {
         tc_fence_before();
@@ -529,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kTok; ++j) {
             if (j >= sg.z) break;
-            const float f = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), sh.sx[buf][j]), sw);
+            const float f = __fmul_rn(__fmul_rn(static_cast<float>(acc[j]), sh.sx[j]), sw);
             if (a.mode == INT8_DOWN) {
-              static_cast<float*>(a.y)[static_cast<int64_t>(sh.slot[buf][j]) * a.n + row] = __fmul_rn(f, sh.tw[buf][j]);
+              static_cast<float*>(a.y)[static_cast<int64_t>(sh.slot[j]) * a.n + row] = __fmul_rn(f, sh.tw[j]);
             } else {
               const float g = f < 0.0f ? 0.0f : f;   // (a NaN stays)
               put_out(a.y, a.mode == INT8_UP ? TQ_DTYPE_BF16 : a.dtype, static_cast<int64_t>(sg.y + j) * a.n + row,
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (w.last_of_segment()) {
-          mbar_arrive(&sh.bempty[buf]);
+          mbar_arrive(&sh.bempty);
           fresh = true;
         }
       }
@@ -566,15 +568,13 @@ cudaError_t launch_as(const CUtensorMap& tw, const Int8StreamArgs& a, int64_t mo
   });
   if (e != cudaSuccess) return e;
   const int part_steps = (a.ksteps + a.parts - 1) / a.parts, b_bytes = part_steps * kTileB;
-  int buffers = 1;
-  if ((a.segs || a.ids) && kSpace - 2 * b_bytes >= 4 * kStageBytes) buffers = 2;
-  int stages = (kSpace - buffers * b_bytes) / kStageBytes;
+  int stages = (kSpace - b_bytes) / kStageBytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (a.parts > 1 && stages >= part_steps) stages = part_steps;   // (none is used again)
   else stages -= stages % kIssuers;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(buffers) * b_bytes + static_cast<size_t>(stages) * kStageBytes + 1024;
+  cfg.dynamicSmemBytes = static_cast<size_t>(b_bytes) + static_cast<size_t>(stages) * kStageBytes + 1024;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -592,10 +592,10 @@ cudaError_t launch_as(const CUtensorMap& tw, const Int8StreamArgs& a, int64_t mo
   cfg.numAttrs = n;
   if (a.parts > 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(a.row_tiles * a.parts));
-    e = cudaLaunchKernelEx(&cfg, int8_stream_kernel<T, true>, tw, a, stages, buffers);
+    e = cudaLaunchKernelEx(&cfg, int8_stream_kernel<T, true>, tw, a, stages);
   } else {
     cfg.gridDim = dim3(static_cast<unsigned>(most_tiles < sms ? most_tiles : sms));
-    e = cudaLaunchKernelEx(&cfg, int8_stream_kernel<T, false>, tw, a, stages, buffers);
+    e = cudaLaunchKernelEx(&cfg, int8_stream_kernel<T, false>, tw, a, stages);
   }
   if (e != cudaSuccess) return e;
   note_launches(1);

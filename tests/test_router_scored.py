@@ -6,6 +6,7 @@ a sum of at most 1024 positive scores of which a lane adds 32 in a row and 5 acr
 two divisions and the scale: (4 + 2) + 37 + 37 + 3 < 90 units of 2^-24, and for softmax the rounding of z - max z,
 |z - max z| <= 20 here, up to 20 more each in the numerator and the sum: 130 * 2^-24 < 8e-6 relative."""
 import ctypes
+import gc
 
 import numpy as np
 import pytest
@@ -200,6 +201,7 @@ def test_strides_streams_graph_and_empty():
     zin = z[:, :128].contiguous()
     bd = b.to(DEV)
     g = torch.cuda.CUDAGraph()
+    gc.collect()                                                   # (a graph freed during a capture ends it)
     with torch.cuda.graph(g):
         out = tq.tq4_1s_router_scored(zin, 6, bias=bd, score="sigmoid")
     zin.copy_(view)
