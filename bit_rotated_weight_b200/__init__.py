@@ -566,47 +566,51 @@ def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | N
         bias = bias.contiguous()
         pb = bias.data_ptr()
     cfg = _router_struct(E, topk, score, num_groups, topk_groups, group_score, renormalize, scale)
-    ids = logits.new_empty((m, max(topk, 0)), dtype=torch.int32)
-    w = logits.new_empty((m, max(topk, 0)), dtype=torch.float32)
+    device = logits.device
+    # (sizes as arguments: a tuple costs half a microsecond more)
+    ids = torch.empty(m, max(topk, 0), dtype=torch.int32, device=device)
+    w = torch.empty(m, max(topk, 0), dtype=torch.float32, device=device)
     rc = load_library().tq4_1s_router_scored(logits.data_ptr(), _DTYPES[dtype], m, cfg, pb, ids.data_ptr(),
-                                             w.data_ptr(), _stream(logits.device))
+                                             w.data_ptr(), _stream(device))
     if rc:
         raise TQ4Error(rc, "router_scored")
     return ids, w
 
 
-@dataclass(frozen=True)
 class Int8Weight:
     """An int8 weight (stack): codes q int8 [E][n][k] and one float32 scale per row, wscale [E][n];
     the weight is wscale[e][i] * q[e][i][j].  The handle is fixed (make a new one for other tensors); the tensors'
     contents may change."""
-    q: torch.Tensor
-    wscale: torch.Tensor
-    n: int
-    k: int
-    num_experts: int
+    __slots__ = ("_q", "_wscale", "_n", "_k", "_num_experts", "_checked")
 
-    @functools.cached_property
-    def _struct(self) -> _Int8Weight:
-        E, n, k = self.num_experts, self.n, self.k
-        if self.q.dtype != torch.int8 or self.q.numel() != E * n * k or not self.q.is_contiguous():
-            raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
-        if self.wscale.dtype != torch.float32 or self.wscale.numel() != E * n or not self.wscale.is_contiguous():
-            raise ValueError("Int8Weight.wscale must be a contiguous float32 tensor of num_experts * n scales")
-        if self.q.device != self.wscale.device or not self.q.is_cuda:
-            raise ValueError("Int8Weight planes must lie on one CUDA device")
-        return _Int8Weight(n, k, E, 0, self.q.data_ptr(), self.wscale.data_ptr())
+    def __init__(self, q: torch.Tensor, wscale: torch.Tensor, n: int, k: int, num_experts: int):
+        self._q, self._wscale, self._n, self._k, self._num_experts, self._checked = q, wscale, n, k, num_experts, None
 
-    @functools.cached_property
-    def device(self) -> torch.device:
-        return self.q.device
+    q = property(lambda self: self._q)
+    wscale = property(lambda self: self._wscale)
+    n = property(lambda self: self._n)
+    k = property(lambda self: self._k)
+    num_experts = property(lambda self: self._num_experts)
+    device = property(lambda self: self._q.device)
+
+    def __repr__(self) -> str:
+        return f"Int8Weight(n={self._n}, k={self._k}, num_experts={self._num_experts}, device={self._q.device})"
 
     def c_struct(self) -> _Int8Weight:
-        return self._struct
+        if self._checked is None:
+            q, s, E, n, k = self._q, self._wscale, self._num_experts, self._n, self._k
+            if q.dtype != torch.int8 or q.numel() != E * n * k or not q.is_contiguous():
+                raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
+            if s.dtype != torch.float32 or s.numel() != E * n or not s.is_contiguous():
+                raise ValueError("Int8Weight.wscale must be a contiguous float32 tensor of num_experts * n scales")
+            if q.device != s.device or not q.is_cuda:
+                raise ValueError("Int8Weight planes must lie on one CUDA device")
+            self._checked = _Int8Weight(n, k, E, 0, q.data_ptr(), s.data_ptr())
+        return self._checked
 
     @property
     def nbytes(self) -> int:
-        return self.q.numel() + self.wscale.numel() * 4
+        return self._q.numel() + self._wscale.numel() * 4
 
 
 def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
@@ -614,17 +618,16 @@ def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
     if _elsewhere(W):
         with torch.cuda.device(W.device):
             return tq4_1s_int8_quantize(W)
-    if W.dim() == 2:
-        W = W.unsqueeze(0)
-    if W.dim() != 3 or not W.is_cuda or W.dtype not in _DTYPES:
+    dtype, dims = _DTYPES.get(W.dtype), W.dim()
+    if dtype is None or (dims != 2 and dims != 3) or not W.is_cuda:
         raise ValueError("W must be a CUDA float32/bfloat16/float16 tensor of shape [n][k] or [E][n][k]")
+    E, (n, k), device = W.shape[0] if dims == 3 else 1, W.shape[-2:], W.device
     W = W.contiguous()
-    E, n, k = W.shape
-    out = Int8Weight(torch.empty((E, n, k), dtype=torch.int8, device=W.device),
-                     torch.empty((E, n), dtype=torch.float32, device=W.device), n, k, E)
-    st = out.c_struct()
-    _check(load_library().tq4_1s_int8_quantize(_ptr(W), _DTYPES[W.dtype], ctypes.byref(st), _stream(W.device)),
-           "int8_quantize")
+    out = Int8Weight(torch.empty(E, n, k, dtype=torch.int8, device=device),
+                     torch.empty(E, n, dtype=torch.float32, device=device), n, k, E)
+    rc = load_library().tq4_1s_int8_quantize(W.data_ptr(), dtype, out.c_struct(), _stream(device))
+    if rc:
+        raise TQ4Error(rc, "int8_quantize")
     return out
 
 
@@ -634,8 +637,10 @@ def tq4_1s_int8_dequantize(w: Int8Weight) -> torch.Tensor:
         with torch.cuda.device(w.q.device):
             return tq4_1s_int8_dequantize(w)
     st = w.c_struct()
-    out = torch.empty((w.num_experts, w.n, w.k), dtype=torch.float32, device=w.q.device)
-    _check(load_library().tq4_1s_int8_dequantize(ctypes.byref(st), _ptr(out), _stream(out.device)), "int8_dequantize")
+    out = torch.empty(w.num_experts, w.n, w.k, dtype=torch.float32, device=w.device)
+    rc = load_library().tq4_1s_int8_dequantize(st, out.data_ptr(), _stream(w.device))
+    if rc:
+        raise TQ4Error(rc, "int8_dequantize")
     return out
 
 
@@ -672,7 +677,7 @@ def tq4_1s_linear_int8(x: torch.Tensor, w: Int8Weight, out: torch.Tensor | None 
     dtype = _DTYPES.get(x.dtype)
     if dtype is None or x.dim() != 2 or not x.is_cuda or x.shape[1] != w.k:
         raise ValueError("x must be a CUDA float32/bfloat16/float16 [m][k] tensor with the weight's k")
-    st = w._struct
+    st = w.c_struct()
     m, device = x.shape[0], x.device
     if w.device != device:
         raise ValueError("x and the weight must lie on one device")
@@ -680,7 +685,7 @@ def tq4_1s_linear_int8(x: torch.Tensor, w: Int8Weight, out: torch.Tensor | None 
     if x.stride(1) != 1 or ldx < w.k:
         x = x.contiguous()
         ldx = w.k
-    out = x.new_empty((m, w.n)) if out is None else _check_out(out, (m, w.n), x.dtype, device)
+    out = x.new_empty(m, w.n) if out is None else _check_out(out, (m, w.n), x.dtype, device)
     ws = size = 0
     if workspace is not None:
         _check_workspace(workspace, device)
@@ -722,12 +727,12 @@ def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
         raise ValueError("topk_ids and topk_w must both be [m][topk]")
     if not (topk_ids.device == topk_w.device == up.device == down.device == device):
         raise ValueError("x, the routing and the weights must lie on one device")
-    u, d = up._struct, down._struct
+    u, d = up.c_struct(), down.c_struct()
     x = x.contiguous()
     topk_ids = topk_ids.to(torch.int32).contiguous()
     topk_w = topk_w.to(torch.float32).contiguous()
     topk = topk_ids.shape[1]
-    out = x.new_empty((m, up.k)) if out is None else _check_out(out, (m, up.k), x.dtype, device)
+    out = x.new_empty(m, up.k) if out is None else _check_out(out, (m, up.k), x.dtype, device)
     if workspace is None:
         size = _moe_int8_bytes(m, topk, (up.n, up.k, up.num_experts), (down.n, down.k, down.num_experts), device.index)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
