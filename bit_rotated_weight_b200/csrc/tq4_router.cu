@@ -202,10 +202,17 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// An expert's choice value in fp64 (softmax's would need its sum; not here).
+// exp(x) or 1 / (1 + exp(-x)), out of line: few rows need it, and code that
+// they alone run has to be fetched first.
+__device__ __noinline__ double exact_score(double x, bool sigmoid) {
+  const double e = exp(sigmoid ? -x : x);
+  return sigmoid ? 1.0 / (1.0 + e) : e;
+}
+// An expert's choice value in fp64 (softmax's with a bias would need its sum;
+// not here).
 template <bool BIASED>
 __device__ __forceinline__ double exact_choice(float z, float b) {
-  return BIASED ? 1.0 / (1.0 + exp(-static_cast<double>(z))) + static_cast<double>(b) : static_cast<double>(z);
+  return BIASED ? exact_score(static_cast<double>(z), true) + static_cast<double>(b) : static_cast<double>(z);
 }
 
 // What a warp keeps from row to row.
@@ -227,16 +234,17 @@ struct Lane {
 // keys) to the lower id.  Each lane keeps its two largest keys; a round takes
 // the largest of the warp and its lane moves on.  The topk + 1 keys taken are
 // in order unless two neighbours are closer than the errors below.
-//   Errors of a value c = s + b against fp64: ex2.approx and rcp.approx 2^-22
-//   and 2^-23 relative, the exponent's rounding |x| 2^-23 in x e^-x terms, the
-//   add of 1: under 5e-7 for sigmoid.  Softmax has the sum's roundings too,
+//   Errors of a value c = s + b against fp64.  Sigmoid: rcp.approx 2^-23 s,
+//   the add of 1 2^-24 s, and through s (1 - s) <= 1/4 ex2.approx's 2^-22 and
+//   the exponent's roundings, |z| 2^-23 (s (1 - s) |z| <= 0.224): under 3e-7.
+//   Softmax has the sum's roundings too,
 //   PL + 5 adds: under (PL + 16) 2^-24.  The bias' add: 2^-24 |c|; the key's
 //   lowest bits: PL 2^-23 |c|.
 // Without a bias the keys are the logits' own, and only the lowest bits go.
 template <typename T, int PL, bool SIGMOID, bool BIASED>
 __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const Lane<PL>& l, float* s_value) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  constexpr float kErr = SIGMOID ? 5e-7f : (PL + 16) * 0x1p-24f;
+  constexpr float kErr = SIGMOID ? 3e-7f : (PL + 16) * 0x1p-24f;
   const int lane = threadIdx.x & 31;
   const T* zt = static_cast<const T*>(a.logits) + t * a.experts;
   const bool grouped = a.keep < a.groups;
@@ -450,10 +458,17 @@ __device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plai
 // Four threads per token, eight tokens a warp: next to no shuffles and no idle
 // lanes.  The rows lie in shared memory; eight experts at a time are turned
 // into keys, sorted by a network and merged into the thread's eight largest,
-// and the four threads' eights at the end.  The keys' lowest bits hold the
-// expert (all ones minus it), which costs more of the value than fast_row's,
-// so about 2 % of the rows are near ties here; the whole warp does those again
-// by fast_row, and by slow_row where that cannot decide either.
+// and the four threads' eights at the end.
+//
+// A key's lowest bits hold the expert (all ones minus it).  Above them stand
+// the highest bits of a logit's own key, or, with a bias, the choice value in
+// fixed point: c + 12 lies in [8, 16) for |c| < 4, so its mantissa counts
+// 2^-20 (of the float's 32 bits those above are the same for all).  A float's
+// own bits, cut to make room for the expert, would count 2^-15 near 1, and
+// 1.5 % of the rows would be near ties; so it is 0.1 %.  Two neighbours that
+// are near are told apart in fp64 in place; what is left (three that are near,
+// groups that are, softmax with a bias) is done again by the whole warp, which
+// costs little work but 10 us of fetching code that is otherwise not run.
 constexpr int kRowsWarps = 2;
 constexpr int kRowsTopk = 8;
 constexpr int kRowsOf = 8;         // tokens of a warp
@@ -474,11 +489,13 @@ __device__ __forceinline__ void sort8(int32_t (&k)[8]) {
   order2(k[2], k[4]), order2(k[3], k[5]);
   order2(k[1], k[2]), order2(k[3], k[4]), order2(k[5], k[6]);
 }
-// Keeps the eight largest of two sorted eights, sorted; `lost` the largest of the rest.
-__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t& lost) {
+// Keeps the eight largest of two sorted eights, sorted; `lost`: the two largest of the rest.
+__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t (&lost)[2]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    lost = max(lost, min(top[i], k[7 - i]));
+    const int32_t out = min(top[i], k[7 - i]);
+    lost[1] = max(lost[1], min(lost[0], out));
+    lost[0] = max(lost[0], out);
     top[i] = max(top[i], k[7 - i]);
   }
 #pragma unroll
@@ -506,7 +523,7 @@ __device__ __forceinline__ float in_shared(const __nv_bfloat16* z) { return __bf
 
 struct RowsShape {
   int pieces, stride;   // 16-byte pieces of a row, and from row to row in shared memory
-  int size, mask;       // experts of a group; the key bits that hold the expert
+  int size, bits, mask; // experts of a group; the key bits that hold the expert
   int bias_floats, warp_bytes;
 };
 template <typename T>
@@ -515,9 +532,9 @@ __host__ __device__ inline RowsShape rows_shape(const RouterArgs& a) {
   s.pieces = a.experts * static_cast<int>(sizeof(T)) / 16;
   s.stride = s.pieces | 1;
   s.size = a.experts / a.groups;
-  s.mask = 1;
-  while (s.mask < a.experts) s.mask *= 2;
-  s.mask -= 1;
+  s.bits = 0;
+  while ((1 << s.bits) < a.experts) ++s.bits;
+  s.mask = (1 << s.bits) - 1;
   // groups' biases lie 4 floats further apart, so that threads at different groups read different banks
   s.bias_floats = a.bias ? a.experts + 4 * a.groups : 0;
   // the rows and their groups' ranks; then, in the same place, what again_row needs
@@ -556,7 +573,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
       const float b = __ldg(a.bias + e);
       s_bias[e + 4 * (e / sh.size)] = b;
-      plain = plain && fabsf(b) < INFINITY;
+      plain = plain && fabsf(b) < 3.0f;   // (for the keys' range; NaN and infinities too)
     }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   plain = __syncthreads_and(plain);
@@ -564,17 +581,17 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
   const T* z = reinterpret_cast<const T*>(tile + own * sh.stride);
   const bool grouped = a.keep < a.groups;
   bool done = plain && own < rows;   // decided here
-  float top2 = 0.0f, inv = 1.0f;
+  float largest = -INFINITY, top2 = 0.0f, inv = 1.0f;   // (softmax)
   if (!SIGMOID) {
-    float top = -INFINITY;
     for (int e = 8 * sub; e < a.experts; e += 32) {
       float v[8];
       eight(z + e, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i]);
+      for (int i = 0; i < 8; ++i) largest = fmaxf(largest, v[i]);
     }
-    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-    top2 = fmaxf(top, __shfl_xor_sync(kAll, top, 2)) * kLog2e;
+    largest = fmaxf(largest, __shfl_xor_sync(kAll, largest, 1));
+    largest = fmaxf(largest, __shfl_xor_sync(kAll, largest, 2));
+    top2 = largest * kLog2e;
     if (BIASED || !a.renorm || (grouped && a.top2)) {
       float sum[2] = {0.0f, 0.0f};
       for (int e = 8 * sub; e < a.experts; e += 32) {
@@ -589,7 +606,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     }
   }
   // (a sum's chain is at most 64 + 3 adds, each relative 2^-24)
-  constexpr float kErr = SIGMOID ? 5e-7f : 80 * 0x1p-24f;
+  constexpr float kErr = SIGMOID ? 3e-7f : 80 * 0x1p-24f;
   auto score = [&](float x) { return SIGMOID ? rcp(1.0f + ex2(x * -kLog2e)) : ex2(fmaf(x, kLog2e, -top2)) * inv; };
   uint32_t kept = 0;
   if (grouped) {
@@ -644,11 +661,54 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
       in = fminf(in, __shfl_xor_sync(kAll, in, o));
       out = fmaxf(out, __shfl_xor_sync(kAll, out, o));
     }
-    if (BIASED || a.top2) done = done && in - out > 4.0f * kErr + 0x1p-21f * fmaxf(fabsf(in), fabsf(out));
+    if (BIASED || a.top2) {
+      // two values' errors in each rank, and the rounding of their sums
+      const float room = 4.0f * kErr + 0x1p-21f * fmaxf(fabsf(in), fabsf(out));
+      const bool unsure = done && !(in - out > room);
+      if (__any_sync(kAll, unsure)) {
+        // the last group kept against the first left out, in fp64
+        int last = -1, first = -1, many = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          const float r = s_rank[g * kRowsOf];
+          if ((kept >> g) & 1u) {
+            if (r <= out + room) last = g, many += 1;
+          } else if (r >= in - room) {
+            first = g, many += 16;
+          }
+        }
+        const bool here = unsure && many == 17 && (SIGMOID || !BIASED);   // (else slow_row's)
+        double rank[2] = {0.0, 0.0};
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int g = here ? (i == 0 ? last : first) : 0;
+          double best = -INFINITY, next = -INFINITY;
+#pragma unroll 1
+          for (int j = sub; here && j < sh.size; j += 4) {
+            const float x = in_shared(z + g * sh.size + j);
+            const double v = exact_score(SIGMOID ? static_cast<double>(x)
+                                                 : static_cast<double>(x) - static_cast<double>(largest), SIGMOID) +
+                             (BIASED ? static_cast<double>(s_bias[g * (sh.size + 4) + j]) : 0.0);
+            next = fmax(next, fmin(best, v));
+            best = fmax(best, v);
+          }
+#pragma unroll 1
+          for (int o = 1; o < 4; o <<= 1) {
+            const double f = __shfl_xor_sync(kAll, best, o), s = __shfl_xor_sync(kAll, next, o);
+            next = fmax(fmin(best, f), fmax(next, s));
+            best = fmax(best, f);
+          }
+          rank[i] = a.top2 ? best + next : best;
+        }
+        if (here && (rank[1] > rank[0] || (rank[1] == rank[0] && first < last))) kept ^= 1u << last | 1u << first;
+        if (unsure && !here) done = false;
+      }
+    }
   } else {
     kept = (a.groups == 32 ? 0u : 1u << a.groups) - 1u;
   }
-  int32_t top[8], lost = kNone;
+  // (nine bits of expert: [16, 24), so that the key keeps its sign bit)
+  const float offset = sh.bits == 9 ? 20.0f : 12.0f;
+  int32_t top[8], lost[2] = {kNone, kNone};
 #pragma unroll
   for (int i = 0; i < 8; ++i) top[i] = kNone;
   bool empty = true;
@@ -665,7 +725,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
       for (int i = 0; i < 8; ++i) {
         if (!grouped) done = done && fabsf(v[i]) < 40.0f;
         const float c = BIASED ? score(v[i]) + b[i] : v[i] + 0.0f;   // (-0 is 0)
-        k[i] = (key_of(c) & ~sh.mask) | (sh.mask - e - i);
+        if (BIASED) k[i] = __float_as_int(c + offset) * (1 << sh.bits) + (sh.mask - e - i);
+        else k[i] = (key_of(c) & ~sh.mask) | (sh.mask - e - i);
       }
       sort8(k);
       if (empty) {
@@ -682,16 +743,18 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     int32_t k[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(kAll, top[i], o);
-    lost = max(lost, __shfl_xor_sync(kAll, lost, o));
+    const int32_t l0 = __shfl_xor_sync(kAll, lost[0], o), l1 = __shfl_xor_sync(kAll, lost[1], o);
+    lost[1] = max(max(lost[1], l1), min(lost[0], l0));
+    lost[0] = max(lost[0], l0);
     merge8(top, k, lost);
   }
   // thread `sub` of the four has the choices sub and sub + 4
   int id[2];
-  bool close[2] = {false, false};
-  auto room = [&](float x, float y) {
-    return BIASED ? 2.0f * kErr + fmaxf(fabsf(x), fabsf(y)) * ((sh.mask + 3) * 0x1p-23f) : 0.0f;
-  };
   auto expert = [&](int32_t key) { return min(sh.mask - (key & sh.mask), a.experts - 1); };
+  // two scores' errors and two roundings, in counts of the fixed point
+  constexpr int kRoom = BIASED ? static_cast<int>(2.0f * kErr * 0x1p20f) + 3 : 0;
+  auto near = [&](int32_t hi, int32_t lo) { return lo != kNone && (hi >> sh.bits) - (lo >> sh.bits) <= kRoom; };
+  bool close[2] = {false, false};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     int32_t key = top[4 * h], after = top[4 * h + 1];
@@ -699,65 +762,59 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     for (int i = 1; i < 4; ++i)
       if (sub == i) {
         key = top[4 * h + i];
-        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost;
+        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost[0];
       }
     id[h] = expert(key);
-    if (BIASED || sizeof(T) == 4) {   // (a bf16 logit's key holds all of it)
-      const float hi = value_of(key & ~sh.mask), lo = value_of(after & ~sh.mask);
-      close[h] = sub + 4 * h < a.topk && after != kNone && !(hi - lo > room(hi, lo));
-    }
+    // (a bf16 logit's key holds all of it)
+    if (BIASED || sizeof(T) == 4) close[h] = sub + 4 * h < a.topk && near(key, after);
   }
   if (BIASED || sizeof(T) == 4) {
-    const uint32_t quad = 15u << (lane & ~3);
-    const uint32_t c0 = __ballot_sync(kAll, close[0] && done), c1 = __ballot_sync(kAll, close[1] && done);
-    if (!SIGMOID && BIASED) {   // (softmax's fp64 sum is slow_row's)
-      if ((c0 | c1) & quad) done = false;
-    } else if (c0 | c1) {
-      // Near ties: the choices and the next expert ranked again by their values
-      // in fp64.  Where the last place is in question, no other expert may be
-      // near it.
-      const int edge = a.topk - 1;
-      const bool last = (((edge < 4 ? c0 : c1) & quad) >> ((lane & ~3) + (edge & 3))) & 1u;
-      int32_t at_edge = top[0], beyond = kNone;
-      int next_id = expert(lost);
+    const uint32_t c[2] = {__ballot_sync(kAll, close[0] && done) >> (lane & ~3) & 15u,
+                           __ballot_sync(kAll, close[1] && done) >> (lane & ~3) & 15u};
+    const uint32_t pairs = c[0] | c[1] << 4;   // bit j: choices j and j + 1 of this row are near
+    if (__any_sync(kAll, pairs != 0)) {
+      // Each such pair by its values in fp64.  Left to fast_row: three in a
+      // row, a last place that two others are near, and two pairs of a thread.
+      int32_t edge = kNone, third = lost[1], next = lost[0];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (i == edge) at_edge = top[i];
-        if (i == a.topk) next_id = expert(top[i]);
-        if (i == a.topk + 1) beyond = top[i];
+        if (i == a.topk - 1) edge = top[i];
+        if (i == a.topk) next = top[i];
+        if (i == a.topk + 1) third = top[i];
       }
-      if (a.topk == 7) beyond = lost;
-      const float e0 = value_of(at_edge & ~sh.mask), e1 = value_of(beyond & ~sh.mask);
-      // (with eight choices the expert after the next is not known)
-      if (last && (a.topk == 8 || (beyond != kNone && !(e0 - e1 > room(e0, e1))))) done = false;
-      // the next expert, at place topk, is every thread's; choices past topk count for nothing
-      auto value = [&](int e) {
-        return exact_choice<BIASED>(in_shared(z + e), BIASED ? s_bias[e + 4 * (e / sh.size)] : 0.0f);
-      };
-      const double c[2] = {value(id[0]), value(id[1])}, cn = value(next_id);
-      int place[2] = {0, 0}, place_n = 0;
-      for (int o = 0; o < a.topk; ++o) {
-        const int from = (lane & ~3) | (o & 3);
-        const double oc = __shfl_sync(kAll, o < 4 ? c[0] : c[1], from);
-        const int oid = __shfl_sync(kAll, o < 4 ? id[0] : id[1], from);
+      if (a.topk == 7) third = lost[0];
+      const bool last = (pairs >> (a.topk - 1)) & 1u;
+      if ((pairs & (pairs << 1)) || (c[0] & c[1]) || (last && near(edge, third)) || (pairs && !SIGMOID && BIASED))
+        done = false;
+      const int h = c[1] && (c[1] >> sub & 1u) ? 1 : 0;
+      bool swap = false;
+      if (done && ((pairs >> (sub + 4 * h)) & 1u)) {
+        int32_t after = next;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) place[h] += (oc > c[h] || (oc == c[h] && oid < id[h])) ? 1 : 0;
-        place_n += (oc > cn || (oc == cn && oid < next_id)) ? 1 : 0;
+        for (int i = 1; i < 8; ++i)
+          if (i == sub + 4 * h + 1 && i < a.topk) after = top[i];
+        const int e[2] = {h ? id[1] : id[0], expert(after)};
+        double v[2];
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i)
+          v[i] = exact_choice<BIASED>(in_shared(z + e[i]) + 0.0f, BIASED ? s_bias[e[i] + 4 * (e[i] / sh.size)] : 0.0f);
+        swap = v[1] > v[0] || (v[1] == v[0] && e[1] < e[0]);
       }
-      if (last)
+      const uint32_t low = __ballot_sync(kAll, swap && h == 0) >> (lane & ~3) & 15u;
+      const uint32_t high = __ballot_sync(kAll, swap && h == 1) >> (lane & ~3) & 15u;
+      const uint32_t swaps = low | high << 4;   // bit j: choices j and j + 1 of this row change places
 #pragma unroll
-        for (int h = 0; h < 2; ++h) place[h] += (cn > c[h] || (cn == c[h] && next_id < id[h])) ? 1 : 0;
-      int new_id[2] = {id[0], id[1]};
-      for (int o = 0; o < a.topk; ++o) {
-        const int from = (lane & ~3) | (o & 3);
-        const int at = __shfl_sync(kAll, o < 4 ? place[0] : place[1], from);
-        const int oid = __shfl_sync(kAll, o < 4 ? id[0] : id[1], from);
+      for (int g = 0; g < 2; ++g) {
+        const int j = sub + 4 * g;
+        int32_t key = kNone;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (at == sub + 4 * h) new_id[h] = oid;
+        for (int i = 0; i < 8; ++i) {
+          if (i == j + 1 && i < a.topk && (swaps >> j & 1u)) key = top[i];
+          if (i + 1 == j && (swaps >> i & 1u)) key = top[i];
+        }
+        if (j == a.topk - 1 && (swaps >> j & 1u)) key = next;
+        if (key != kNone) id[g] = expert(key);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) id[h] = last && place_n == sub + 4 * h ? next_id : new_id[h];
     }
   }
   float w[2];

@@ -335,3 +335,23 @@ def test_near_ties_of_many_rows(m, topk):
     z = (z.view(np.int32) + rng.integers(0, 3, z.shape).astype(np.int32) * (z != 0)).view(np.float32)
     check(torch.from_numpy(z).to(DEV), topk, None, "sigmoid", 8, 3, "max")
     check(torch.from_numpy(z).to(DEV), topk, None, "softmax")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("m", [40, 1500])
+def test_near_ties_of_groups(m, group_score):
+    # groups made of the same few logits and of biases that differ by 2^-22 .. 2^-30: their ranks are near, or equal
+    E, G = 128, 8
+    rng = np.random.default_rng(m)
+    z = np.tile((rng.integers(-4, 5, (m, 1, 16)) / 4), (1, G, 1)).reshape(m, E).astype(np.float32)
+    b = np.tile(rng.integers(0, 3, 16) * 0.125, G) + np.repeat(rng.integers(0, 2, G) * 2.0 ** -rng.integers(22, 31, G), 16)
+    b = torch.from_numpy(b.astype(np.float32))
+    for score in ("sigmoid", "softmax"):
+        for keep in (1, 4, 7):
+            check(torch.from_numpy(z).to(DEV), 6, b, score, G, keep, group_score)
+            check(torch.from_numpy(z).to(DEV), 6, None, score, G, keep, group_score)
+    # two of the groups only
+    z[:, 32:] -= rng.random((m, E - 32)).astype(np.float32) + 2
+    for score in ("sigmoid", "softmax"):
+        check(torch.from_numpy(z).to(DEV), 6, b, score, G, 1, group_score)
