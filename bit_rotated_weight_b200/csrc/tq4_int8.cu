@@ -397,6 +397,8 @@ int weight_ok(const tq4_1s_int8_weight* w, bool need_ptrs) {
   return TQ_OK;
 }
 
+constexpr int64_t kMaxTiles = 1 << 30;
+
 // How a dense product is run: tokens a tile, CTAs.
 struct Plan {
   int nt, grid;
@@ -560,7 +562,12 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   int sms = 0;
   if ((rc = check_device(&sms))) return rc;
   const Plan p = plan_dense(m, w->n, w->k, sms);
-  if (p.row_tiles * p.tok_tiles > INT32_MAX / p.ksteps) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  if (p.row_tiles * p.tok_tiles > kMaxTiles) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  const int64_t bytes = dtype == TQ_DTYPE_F32 ? 4 : 2;
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+  if (x0 < y0 + static_cast<uintptr_t>(m * w->n * bytes) &&
+      y0 < x0 + static_cast<uintptr_t>(((m - 1) * ldx + w->k) * bytes))
+    return TQ_ERR_INVALID_ARG;   // y over x: other CTAs may still read x when the first write y
   const bool stream_rows = streams(m, w->k);
   const LinearLayout L = linear_layout(m, w->k);
   if (!stream_rows && (!ws || ws_bytes < L.total)) return TQ_ERR_WORKSPACE;
@@ -633,7 +640,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   const int64_t H = up->k, I = up->n, E = up->num_experts;
   const MoeLayout L = moe_layout(m, topk, E, H, I);
   const int64_t rt_up = (I + 127) / 128, rt_dn = (H + 127) / 128;
-  if (L.maxseg * rt_up > INT32_MAX || L.maxseg * rt_dn > INT32_MAX) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
+  if (L.maxseg * rt_up > kMaxTiles || L.maxseg * rt_dn > kMaxTiles) return TQ_ERR_INVALID_ARG;   // 32-bit tile numbers
   if (!ws || ws_bytes < L.total) return TQ_ERR_WORKSPACE;
   if (!aligned16(ws)) return TQ_ERR_ALIGNMENT;
   if (take_injected_failure()) return TQ_ERR_CUDA;

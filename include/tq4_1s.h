@@ -400,7 +400,7 @@ size_t tq4_1s_linear_int8_workspace(int64_t m, const tq4_1s_int8_weight* w);
  * one rounding to T at the end; no bias.
  *   x   device [m] rows of k elements, dtype F32, BF16 or F16, rows ldx >= k
  *       elements apart, aligned to its elements;
- *   y   device [m][n] of the same dtype, 16-byte aligned;
+ *   y   device [m][n] of the same dtype, 16-byte aligned, not over x;
  *   ws  device workspace of tq4_1s_linear_int8_workspace(m, w) bytes, 16-byte
  *       aligned; it needs no initialisation, and calls that share one must not
  *       overlap on the GPU.

@@ -7,6 +7,9 @@ the output's type."""
 import contextlib
 import ctypes
 import gc
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -312,6 +315,28 @@ def test_linear_streams_graphs_and_workspaces():
 
 
 @pytest.mark.gpu
+def test_linear_offsets_past_32_bits():
+    # 2.2e9 outputs: the last rows of a batch against the same rows on their own
+    w, q, s = weight(33000, 32, 90)
+    x = torch.randn(66000, 32, generator=gen(91)).half().to(DEV)
+    y = tq.tq4_1s_linear_int8(x, w)
+    for rows in (slice(0, 9), slice(65000, 65009), slice(65990, 66000), slice(65000, 65300)):
+        assert torch.equal(bits(y[rows]), bits(tq.tq4_1s_linear_int8(x[rows], w)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [3, 100])
+def test_linear_refuses_an_output_over_its_input(m):
+    w, _, _ = weight(64, 64, 92)
+    buf = torch.zeros(2 * m * 64, dtype=BF16, device=DEV)
+    x = buf[:m * 64].view(m, 64)
+    for out in (x, buf[8:8 + m * 64].view(m, 64)):
+        with pytest.raises(tq.TQ4Error, match=r"code 1\)"):
+            tq.tq4_1s_linear_int8(x, w, out=out)
+    assert tq.tq4_1s_linear_int8(x, w, out=buf[m * 64:].view(m, 64)).shape == (m, 64)
+
+
+@pytest.mark.gpu
 def test_linear_right_after_its_weight_is_written():
     # the weight's quantizer, the product and the next weight's quantizer into the same planes, back to back
     x = torch.randn(16, 1024, generator=gen(30)).to(BF16).to(DEV)
@@ -382,7 +407,7 @@ def routing(m, E, topk, seed):
 @pytest.mark.parametrize("m,E,topk,H,I,dtype", [
     (1, 8, 2, 256, 128, BF16), (1, 128, 6, 160, 96, BF16), (4, 1, 1, 64, 32, F16), (16, 32, 6, 512, 256, BF16),
     (33, 8, 3, 96, 416, F16), (64, 4, 4, 288, 160, BF16), (200, 8, 2, 256, 224, BF16), (500, 5, 3, 128, 192, F16),
-    (1500, 4, 2, 64, 320, BF16), (3, 300, 64, 64, 64, BF16), (40, 1100, 4, 32, 64, BF16),
+    (1500, 4, 2, 64, 320, BF16), (3, 300, 64, 64, 64, BF16), (40, 1100, 4, 32, 64, BF16), (2, 8, 2, 9248, 64, BF16),
 ])
 def test_moe_matches_plain(m, E, topk, H, I, dtype):
     up, down, ru, rd = moe_weights(E, H, I, m + E)
@@ -407,6 +432,20 @@ def test_moe_all_tokens_at_one_expert_and_repeated_ids(m):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("m", [40, 64, 300])
+def test_moe_many_experts_and_all_tokens_at_one(m):
+    # few rows an expert on the mean, and all of them at one: segments of 16 of its rows
+    up, down, ru, rd = moe_weights(700, 64, 96, 41)
+    x = torch.randn(m, 64, generator=gen(m)).to(BF16)
+    ids = np.full((m, 2), 699, np.int32)
+    tw = np.random.default_rng(m).standard_normal((m, 2)).astype(np.float32)
+    check_moe(x, ids, tw, up, down, ru, rd)
+    ids[::3, 0] = 0
+    ids[1::5, 1] = -1
+    check_moe(x, ids, tw, up, down, ru, rd)
+
+
+@pytest.mark.gpu
 def test_moe_bad_ids_are_skipped_and_flagged():
     up, down, ru, rd = moe_weights(8, 128, 96, 42)
     ids, tw = routing(30, 8, 3, 43)
@@ -420,6 +459,69 @@ def test_moe_bad_ids_are_skipped_and_flagged():
     y = tq.tq4_1s_moe_int8(x.to(DEV), torch.full((30, 3), -1, dtype=torch.int32, device=DEV),
                            torch.from_numpy(tw).to(DEV), up, down)
     assert bool((y == 0).all()) and tq.tq4_1s_get_status() == tq.TQ_DEV_BAD_ROUTING
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,E", [(2, 32), (30, 200), (60, 8)])
+def test_moe_tokens_and_routing_off_alignment(m, E):
+    # slices that start at odd places, ids as int64, a token's ids in a wider matrix
+    up, down, ru, rd = moe_weights(E, 96, 64, 93)
+    ids, tw = routing(m, E, 3, 94)
+    x = torch.randn(m, 96, generator=gen(95)).to(BF16)
+    buf = torch.zeros(m * 96 + 3, dtype=BF16, device=DEV)
+    view = buf[3:].view(m, 96)
+    view.copy_(x)
+    wide = torch.zeros(m, 5, dtype=torch.int64, device=DEV)
+    wide[:, 1:4] = torch.from_numpy(ids).to(DEV)
+    tbuf = torch.zeros(m * 3 + 1, device=DEV)
+    tbuf[1:] = torch.from_numpy(tw).to(DEV).flatten()
+    y = tq.tq4_1s_moe_int8(view, wide[:, 1:4], tbuf[1:].view(m, 3), up, down)
+    y32, _, _ = ref_moe(x, ids, tw, ru, rd)
+    assert torch.equal(bits(y), bits(torch.from_numpy(y32).to(BF16)))
+
+
+@pytest.mark.gpu
+def test_moe_in_place():
+    up, down, ru, rd = moe_weights(8, 128, 96, 96)
+    for m in (2, 40):                                      # x is read before y is written
+        ids, tw = routing(m, 8, 2, 97)
+        x = torch.randn(m, 128, generator=gen(98)).to(BF16)
+        want = check_moe(x, ids, tw, up, down, ru, rd)
+        xd = x.to(DEV)
+        tq.tq4_1s_moe_int8(xd, torch.from_numpy(ids).to(DEV), torch.from_numpy(tw).to(DEV), up, down, out=xd)
+        assert torch.equal(bits(xd), bits(want))
+
+
+@pytest.mark.gpu
+def test_first_calls_of_a_process_may_be_captured():
+    code = """
+import torch, bit_rotated_weight_b200 as tq
+d = 'cuda'
+w = tq.Int8Weight(torch.ones(1, 4096, 64, dtype=torch.int8, device=d), torch.ones(1, 4096, device=d), 4096, 64, 1)
+up = tq.Int8Weight(torch.ones(4, 64, 96, dtype=torch.int8, device=d), torch.full((4, 64), 1e-3, device=d), 64, 96, 4)
+dn = tq.Int8Weight(torch.ones(4, 96, 64, dtype=torch.int8, device=d), torch.full((4, 96), 1e-3, device=d), 96, 64, 4)
+xs = [torch.ones(m, 64, device=d) for m in (4, 100, 2500)]
+xm = [torch.ones(m, 96, device=d, dtype=torch.bfloat16) for m in (1, 40, 600)]
+z = [torch.randn(m, 4, device=d) for m in (1, 40, 600)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ys = [tq.tq4_1s_linear_int8(x, w) for x in xs]
+    rs = [tq.tq4_1s_router_scored(t, 2, score='sigmoid') for t in z]
+    ms = [tq.tq4_1s_moe_int8(x, i, t, up, dn) for x, (i, t) in zip(xm, rs)]
+    q = tq.tq4_1s_int8_dequantize(tq.tq4_1s_int8_quantize(xs[1]))
+g.replay()
+torch.cuda.synchronize()
+assert all(bool((y == 64.0).all()) for y in ys), [float(y.flatten()[0]) for y in ys]
+for x, (i, t), y, zz in zip(xm, rs, ms, z):
+    assert torch.equal(y, tq.tq4_1s_moe_int8(x, i, t, up, dn))
+    assert all(torch.equal(a, b) for a, b in zip((i, t), tq.tq4_1s_router_scored(zz, 2, score='sigmoid')))
+assert bool((q == 1.0).all())
+print('captured')
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.gpu
@@ -620,7 +722,8 @@ def test_moe_few_rows_an_expert_back_to_back(E, topk, H, I, m, calls):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m,n,k", [(16, 40000, 2688), (1, 20000, 4096), (7, 2048, 8192), (16, 256, 9216)])
+@pytest.mark.parametrize("m,n,k", [(16, 40000, 2688), (1, 20000, 4096), (7, 2048, 8192), (16, 256, 9216),
+                                   (16, 19200, 9216), (9, 19000, 32)])
 def test_linear_few_tokens_back_to_back(m, n, k):
     w, q, s = weight(n, k, 83) if n * k < 1 << 25 else (None, None, None)
     if w is None:                                       # too large for numpy: three row blocks are compared
