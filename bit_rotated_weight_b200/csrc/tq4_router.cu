@@ -2,12 +2,14 @@
 // a balance bias that takes part in the choice only, groups of experts of
 // which the best are kept, top-k, renormalised and scaled weights.
 //
-// One warp per token; lane l holds the experts l, l + 32, ...  The choice is
+// Up to 255 tokens: a warp each, lane l with the experts l, l + 32, ...; more:
+// four threads each (router_rows_kernel).  The choice is
 // that of fp64 scores, but nearly every row is decided in fp32 (see
 // fast_row): errors of the fp32 scores are bounded, and only where two experts
 // or groups that the choice turns on lie closer than that bound is the row
 // done again in fp64 (slow_row).  fp64 scores for every expert took 251 us
-// for 65536 tokens x 256 experts, at 64 fp64 lanes an SM.
+// for 65536 tokens x 256 experts (34 MB), at 64 fp64 lanes an SM; this takes 34
+// us, bound by the issue of about 300 instructions a token.  One token: 3 us.
 #include "tq4_internal.h"
 
 #define TQ_API extern "C" __attribute__((visibility("default")))
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
       const float b = __ldg(a.bias + e);
       s_bias[e + 4 * (e / sh.size)] = b;
-      plain = plain && fabsf(b) < 3.0f;   // (for the keys' range; NaN and infinities too)
+      plain = plain && fabsf(b) <= 2.5f;   // (for the keys' range: 1 + 3 may round to 4; NaN and infinities too)
     }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   plain = __syncthreads_and(plain);
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
       for (int i = 0; i < 8; ++i) {
         if (!grouped) done = done && fabsf(v[i]) < 40.0f;
         const float c = BIASED ? score(v[i]) + b[i] : v[i] + 0.0f;   // (-0 is 0)
-        if (BIASED) k[i] = __float_as_int(c + offset) * (1 << sh.bits) + (sh.mask - e - i);
+        if (BIASED) k[i] = static_cast<int32_t>(__float_as_uint(c + offset) << sh.bits) + (sh.mask - e - i);
         else k[i] = (key_of(c) & ~sh.mask) | (sh.mask - e - i);
       }
       sort8(k);

@@ -355,3 +355,19 @@ def test_near_ties_of_groups(m, group_score):
     z[:, 32:] -= rng.random((m, E - 32)).astype(np.float32) + 2
     for score in ("sigmoid", "softmax"):
         check(torch.from_numpy(z).to(DEV), 6, b, score, G, 1, group_score)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [128, 256, 512])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("edge", [2.5, 3.0, 4.0])
+def test_largest_biases_of_many_rows(E, score, edge):
+    # choice values next to 4, and biases next to where the keys in fixed point end
+    m = 300
+    z = logits(m, E, E, torch.bfloat16)
+    z[:, 5], z[:, E // 2] = 39.0, 4.0
+    b = torch.zeros(E)
+    b[5] = float(np.nextafter(np.float32(edge), np.float32(0)))
+    b[9] = -b[5]
+    check(z, 8, b, score)
+    check(z, 8, b, score, 4, 2, "top2")
