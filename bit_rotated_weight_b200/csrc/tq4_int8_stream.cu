@@ -31,6 +31,13 @@
 // Role loops are not unrolled: a call of a few microseconds runs most of the
 // code once, and fetching instructions was most of its time.
 // Every wait on an mbarrier is bounded.
+//
+// Measured: 16 x 4096 x 4096 9.4 us a call in a graph, 1 x 4096 x 2688 7.2 us
+// (17 and 11 MB: 2.6 and 1.7 us of DRAM), a chain of latencies: the launch 2,
+// the tokens' loads 1.2, their maxima across the cluster 1, codes 0.5 to 1, the
+// MMAs 0.8, the exchange of sums 0.7.  The two projections of 16 tokens x 6 of
+// 128 experts (686 MB) 117 us, 5.9 TB/s, DRAM; those of one token (60 MB)
+// 16 us, 90 and 126 tiles for 148 SMs at 41 GB/s each.
 #include "tq4_int8_mma.cuh"
 #include "tq4_int8_rows.cuh"
 
