@@ -8,8 +8,8 @@
 // fast_row): errors of the fp32 scores are bounded, and only where two experts
 // or groups that the choice turns on lie closer than that bound is the row
 // done again in fp64 (slow_row).  fp64 scores for every expert took 251 us
-// for 65536 tokens x 256 experts (34 MB), at 64 fp64 lanes an SM; this takes 34
-// us, bound by the issue of about 300 instructions a token.  One token: 3 us.
+// for 65536 tokens x 256 experts (34 MB), at 64 fp64 lanes an SM; this takes 28
+// us, bound by the integer units and the issue of about 300 instructions a token.  One token: 3 us.
 #include "tq4_internal.h"
 
 #define TQ_API extern "C" __attribute__((visibility("default")))
@@ -491,20 +491,34 @@ __device__ __forceinline__ void sort8(int32_t (&k)[8]) {
   order2(k[2], k[4]), order2(k[3], k[5]);
   order2(k[1], k[2]), order2(k[3], k[4]), order2(k[5], k[6]);
 }
-// Keeps the eight largest of two sorted eights, sorted; `lost`: the two largest of the rest.
-__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t (&lost)[2]) {
+// Keeps the eight largest of two sorted eights, sorted; `lost`: the largest of the rest.
+__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t& lost) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int32_t out = min(top[i], k[7 - i]);
-    lost[1] = max(lost[1], min(lost[0], out));
-    lost[0] = max(lost[0], out);
+  for (int i = 0; i < 8; i += 2) {
+    lost = max(lost, max(min(top[i], k[7 - i]), min(top[i + 1], k[6 - i])));
     top[i] = max(top[i], k[7 - i]);
+    top[i + 1] = max(top[i + 1], k[6 - i]);
   }
 #pragma unroll
   for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (!(i & d)) order2(top[i], top[i + d]);
+}
+
+// The two largest of (first, second) and eight more.
+__device__ __forceinline__ void two_of_eight(const float (&v)[8], float& first, float& second) {
+  float hi[4], lo[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    hi[i] = fmaxf(v[2 * i], v[2 * i + 1]);
+    lo[i] = fminf(v[2 * i], v[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    second = fmaxf(fmaxf(second, lo[i]), fminf(first, hi[i]));
+    first = fmaxf(first, hi[i]);
+  }
 }
 
 __device__ __forceinline__ void eight(const float* z, float (&v)[8]) {
@@ -526,14 +540,16 @@ __device__ __forceinline__ float in_shared(const __nv_bfloat16* z) { return __bf
 struct RowsShape {
   int pieces, stride;   // 16-byte pieces of a row, and from row to row in shared memory
   int size, bits, mask; // experts of a group; the key bits that hold the expert
+  float per_size;       // 1 / size
   int bias_floats, warp_bytes;
 };
 template <typename T>
-__host__ __device__ inline RowsShape rows_shape(const RouterArgs& a) {
+RowsShape rows_shape(const RouterArgs& a) {
   RowsShape s;
   s.pieces = a.experts * static_cast<int>(sizeof(T)) / 16;
   s.stride = s.pieces | 1;
   s.size = a.experts / a.groups;
+  s.per_size = 1.0f / static_cast<float>(s.size);
   s.bits = 0;
   while ((1 << s.bits) < a.experts) ++s.bits;
   s.mask = (1 << s.bits) - 1;
@@ -546,10 +562,10 @@ __host__ __device__ inline RowsShape rows_shape(const RouterArgs& a) {
 }
 
 template <typename T, bool SIGMOID, bool BIASED>
-__global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const __grid_constant__ RouterArgs a) {
+__global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const __grid_constant__ RouterArgs a,
+                                                                         const __grid_constant__ RowsShape sh) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   extern __shared__ uint4 s_rows[];
-  const RowsShape sh = rows_shape<T>(a);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3, own = lane >> 2;
   float* s_bias = reinterpret_cast<float*>(s_rows);
   uint8_t* mine = reinterpret_cast<uint8_t*>(s_rows) + sh.bias_floats * 4 + warp * sh.warp_bytes;
@@ -574,7 +590,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
   if (BIASED)
     for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
       const float b = __ldg(a.bias + e);
-      s_bias[e + 4 * (e / sh.size)] = b;
+      s_bias[e + 4 * static_cast<int>((e + 0.5f) * sh.per_size)] = b;   // (e / size)
       plain = plain && fabsf(b) <= 2.5f;   // (for the keys' range: 1 + 3 may round to 4; NaN and infinities too)
     }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -611,34 +627,34 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
   constexpr float kErr = SIGMOID ? 3e-7f : 80 * 0x1p-24f;
   auto score = [&](float x) { return SIGMOID ? rcp(1.0f + ex2(x * -kLog2e)) : ex2(fmaf(x, kLog2e, -top2)) * inv; };
   uint32_t kept = 0;
+  float squares = 0.0f;   // of the logits seen
   if (grouped) {
-    for (int g = 0; g < a.groups; ++g) {
+    // a group to a thread, or where their number does not suit that to all
+    // four (65536 x 256 in 8 groups: 30.3 us, 33.0 by all four)
+    const bool alone = a.groups % 4 == 0;
+    for (int g = alone ? sub : 0; g < a.groups; g += alone ? 4 : 1) {
       float first = -INFINITY, second = -INFINITY;
-      for (int j = 8 * sub; j < sh.size; j += 32) {
+      for (int j = alone ? 0 : 8 * sub; j < sh.size; j += alone ? 8 : 32) {
         float v[8];
         eight(z + g * sh.size + j, v);
-        // beyond 40 an fp32 weight may underflow where its fp64 form does not
 #pragma unroll
-        for (int i = 0; i < 8; ++i) done = done && fabsf(v[i]) < 40.0f;   // (not of a NaN)
+        for (int i = 0; i < 8; ++i) squares = fmaf(v[i], v[i], squares);
         if (BIASED || a.top2) {
           float b[8];
           if (BIASED) eight(s_bias + g * (sh.size + 4) + j, b);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = BIASED ? score(v[i]) + b[i] : score(v[i]);
         }
+        two_of_eight(v, first, second);
+      }
+      if (!alone)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          second = fmaxf(second, fminf(first, v[i]));
-          first = fmaxf(first, v[i]);
+        for (int o = 1; o < 4; o <<= 1) {
+          const float f = __shfl_xor_sync(kAll, first, o), s = __shfl_xor_sync(kAll, second, o);
+          second = fmaxf(fminf(first, f), fmaxf(second, s));
+          first = fmaxf(first, f);
         }
-      }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        const float f = __shfl_xor_sync(kAll, first, o), s = __shfl_xor_sync(kAll, second, o);
-        second = fmaxf(fminf(first, f), fmaxf(second, s));
-        first = fmaxf(first, f);
-      }
-      if (sub == 0) s_rank[g * kRowsOf] = a.top2 ? first + second : first;
+      if (alone || sub == 0) s_rank[g * kRowsOf] = a.top2 ? first + second : first;
     }
     __syncwarp();
     float in = INFINITY, out = -INFINITY;
@@ -710,7 +726,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
   }
   // (nine bits of expert: [16, 24), so that the key keeps its sign bit)
   const float offset = sh.bits == 9 ? 20.0f : 12.0f;
-  int32_t top[8], lost[2] = {kNone, kNone};
+  const uint32_t unit = sh.mask + 1;   // (a multiply-add: not the integer units' work)
+  auto key_at = [&](float x, float b, int e) {
+    const float c = BIASED ? score(x) + b : x + 0.0f;   // (-0 is 0)
+    if (BIASED) return static_cast<int32_t>(__float_as_uint(c + offset) * unit + static_cast<uint32_t>(sh.mask - e));
+    return (key_of(c) & ~sh.mask) | (sh.mask - e);
+  };
+  int32_t top[8], lost = kNone;
+  const uint32_t stay = kept;
 #pragma unroll
   for (int i = 0; i < 8; ++i) top[i] = kNone;
   bool empty = true;
@@ -725,10 +748,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
       int32_t k[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (!grouped) done = done && fabsf(v[i]) < 40.0f;
-        const float c = BIASED ? score(v[i]) + b[i] : v[i] + 0.0f;   // (-0 is 0)
-        if (BIASED) k[i] = static_cast<int32_t>(__float_as_uint(c + offset) << sh.bits) + (sh.mask - e - i);
-        else k[i] = (key_of(c) & ~sh.mask) | (sh.mask - e - i);
+        if (!grouped) squares = fmaf(v[i], v[i], squares);
+        k[i] = key_at(v[i], BIASED ? b[i] : 0.0f, e + i);
       }
       sort8(k);
       if (empty) {
@@ -740,14 +761,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
       }
     }
   }
+  // Beyond 40 an fp32 weight may underflow where its fp64 form does not.  (The
+  // sum of squares leaves the integer units, which bound this kernel, alone.)
+  if (__any_sync(kAll, !(squares < 1600.0f)))
+    for (int e = sub; e < a.experts; e += 4) done = done && fabsf(in_shared(z + e)) < 40.0f;   // (not of a NaN)
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     int32_t k[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(kAll, top[i], o);
-    const int32_t l0 = __shfl_xor_sync(kAll, lost[0], o), l1 = __shfl_xor_sync(kAll, lost[1], o);
-    lost[1] = max(max(lost[1], l1), min(lost[0], l0));
-    lost[0] = max(lost[0], l0);
+    lost = max(lost, __shfl_xor_sync(kAll, lost, o));
     merge8(top, k, lost);
   }
   // thread `sub` of the four has the choices sub and sub + 4
@@ -764,7 +787,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     for (int i = 1; i < 4; ++i)
       if (sub == i) {
         key = top[4 * h + i];
-        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost[0];
+        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost;
       }
     id[h] = expert(key);
     // (a bf16 logit's key holds all of it)
@@ -777,15 +800,31 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 10) router_rows_kernel(const 
     if (__any_sync(kAll, pairs != 0)) {
       // Each such pair by its values in fp64.  Left to fast_row: three in a
       // row, a last place that two others are near, and two pairs of a thread.
-      int32_t edge = kNone, third = lost[1], next = lost[0];
+      int32_t edge = kNone, third = lost, next = lost;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (i == a.topk - 1) edge = top[i];
         if (i == a.topk) next = top[i];
         if (i == a.topk + 1) third = top[i];
       }
-      if (a.topk == 7) third = lost[0];
       const bool last = (pairs >> (a.topk - 1)) & 1u;
+      if (a.topk == 8 && __any_sync(kAll, last)) {   // the largest below `next` was not kept
+        third = kNone;
+        uint32_t left = stay;
+#pragma unroll 1
+        for (int n = 0; n < a.keep; ++n) {
+          const int g = left ? __ffs(left) - 1 : 0;
+          left &= left - 1;
+#pragma unroll 1
+          for (int j = sub; j < sh.size; j += 4) {
+            const int e = g * sh.size + j;
+            const int32_t k = key_at(in_shared(z + e), BIASED ? s_bias[e + 4 * g] : 0.0f, e);
+            if (k < next) third = max(third, k);
+          }
+        }
+        third = max(third, __shfl_xor_sync(kAll, third, 1));
+        third = max(third, __shfl_xor_sync(kAll, third, 2));
+      }
       if ((pairs & (pairs << 1)) || (c[0] & c[1]) || (last && near(edge, third)) || (pairs && !SIGMOID && BIASED))
         done = false;
       const int h = c[1] && (c[1] >> sub & 1u) ? 1 : 0;
@@ -902,7 +941,7 @@ cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
   const RowsShape s = rows_shape<T>(a);
   const int64_t rows = kRowsOf * kRowsWarps;
   router_rows_kernel<T, SIGMOID, BIASED><<<static_cast<unsigned>((a.m + rows - 1) / rows), kRowsWarps * 32,
-                                           s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st>>>(a);
+                                           s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st>>>(a, s);
   note_launches(1);
   return cudaGetLastError();
 }
