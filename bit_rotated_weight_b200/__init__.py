@@ -581,10 +581,11 @@ class Int8Weight:
     """An int8 weight (stack): codes q int8 [E][n][k] and one float32 scale per row, wscale [E][n];
     the weight is wscale[e][i] * q[e][i][j].  The handle is fixed (make a new one for other tensors); the tensors'
     contents may change."""
-    __slots__ = ("_q", "_wscale", "_n", "_k", "_num_experts", "_checked")
+    __slots__ = ("_q", "_wscale", "_n", "_k", "_num_experts", "_sizes", "_index", "_checked")
 
     def __init__(self, q: torch.Tensor, wscale: torch.Tensor, n: int, k: int, num_experts: int):
         self._q, self._wscale, self._n, self._k, self._num_experts, self._checked = q, wscale, n, k, num_experts, None
+        self._sizes, self._index = (n, k, num_experts), q.get_device()
 
     q = property(lambda self: self._q)
     wscale = property(lambda self: self._wscale)
@@ -675,23 +676,23 @@ def tq4_1s_linear_int8(x: torch.Tensor, w: Int8Weight, out: torch.Tensor | None 
         with torch.cuda.device(x.device):
             return tq4_1s_linear_int8(x, w, out, workspace)
     dtype = _DTYPES.get(x.dtype)
-    if dtype is None or x.dim() != 2 or not x.is_cuda or x.shape[1] != w.k:
+    if dtype is None or x.dim() != 2 or not x.is_cuda or x.shape[1] != w._k:
         raise ValueError("x must be a CUDA float32/bfloat16/float16 [m][k] tensor with the weight's k")
     st = w.c_struct()
     m, device = x.shape[0], x.device
-    if w.device != device:
+    if w._index != x.get_device():
         raise ValueError("x and the weight must lie on one device")
     ldx = x.stride(0)
-    if x.stride(1) != 1 or ldx < w.k:
+    if x.stride(1) != 1 or ldx < w._k:
         x = x.contiguous()
-        ldx = w.k
-    out = x.new_empty(m, w.n) if out is None else _check_out(out, (m, w.n), x.dtype, device)
+        ldx = w._k
+    out = x.new_empty(m, w._n) if out is None else _check_out(out, (m, w._n), x.dtype, device)
     ws = size = 0
     if workspace is not None:
         _check_workspace(workspace, device)
         ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        need = _linear_int8_bytes(m, w.n, w.k, w.num_experts, device.index)
+        need = _linear_int8_bytes(m, w._n, w._k, w._num_experts, w._index)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
             ws, size = workspace.data_ptr(), need
@@ -708,8 +709,7 @@ def _moe_int8_bytes(m: int, topk: int, up: tuple, down: tuple, device: int) -> i
 
 
 def tq4_1s_moe_int8_workspace(m: int, topk: int, up: Int8Weight, down: Int8Weight) -> int:
-    return _moe_int8_bytes(m, topk, (up.n, up.k, up.num_experts), (down.n, down.k, down.num_experts),
-                           up.q.device.index)
+    return _moe_int8_bytes(m, topk, up._sizes, down._sizes, up._index)
 
 
 def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, up: Int8Weight, down: Int8Weight,
@@ -720,26 +720,30 @@ def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     if _elsewhere(x):
         with torch.cuda.device(x.device):
             return tq4_1s_moe_int8(x, topk_ids, topk_w, up, down, out, workspace)
-    if x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float16) or x.shape[1] != up.k:
+    dtype = x.dtype
+    if x.dim() != 2 or not x.is_cuda or (dtype != torch.bfloat16 and dtype != torch.float16) or x.shape[1] != up._k:
         raise ValueError("x must be a CUDA bfloat16/float16 [m][H] tensor with the up projection's k")
-    m, device = x.shape[0], x.device
+    m, device, index = x.shape[0], x.device, x.get_device()
     if topk_ids.dim() != 2 or topk_ids.shape[0] != m or topk_w.shape != topk_ids.shape:
         raise ValueError("topk_ids and topk_w must both be [m][topk]")
-    if not (topk_ids.device == topk_w.device == up.device == down.device == device):
-        raise ValueError("x, the routing and the weights must lie on one device")
     u, d = up.c_struct(), down.c_struct()
+    if not (topk_ids.get_device() == topk_w.get_device() == up._index == down._index == index):
+        raise ValueError("x, the routing and the weights must lie on one device")
     x = x.contiguous()
-    topk_ids = topk_ids.to(torch.int32).contiguous()
-    topk_w = topk_w.to(torch.float32).contiguous()
+    if topk_ids.dtype != torch.int32:   # (a conversion to its own type costs half a microsecond)
+        topk_ids = topk_ids.to(torch.int32)
+    if topk_w.dtype != torch.float32:
+        topk_w = topk_w.to(torch.float32)
+    topk_ids, topk_w = topk_ids.contiguous(), topk_w.contiguous()
     topk = topk_ids.shape[1]
-    out = x.new_empty(m, up.k) if out is None else _check_out(out, (m, up.k), x.dtype, device)
+    out = x.new_empty(m, up._k) if out is None else _check_out(out, (m, up._k), dtype, device)
     if workspace is None:
-        size = _moe_int8_bytes(m, topk, (up.n, up.k, up.num_experts), (down.n, down.k, down.num_experts), device.index)
+        size = _moe_int8_bytes(m, topk, up._sizes, down._sizes, index)
         workspace = torch.empty(size, dtype=torch.uint8, device=device)
     else:
         _check_workspace(workspace, device)
         size = workspace.numel() * workspace.element_size()
-    rc = load_library().tq4_1s_moe_int8(x.data_ptr(), _DTYPES[x.dtype], m, topk_ids.data_ptr(), topk_w.data_ptr(),
+    rc = load_library().tq4_1s_moe_int8(x.data_ptr(), _DTYPES[dtype], m, topk_ids.data_ptr(), topk_w.data_ptr(),
                                         topk, u, d, out.data_ptr(), workspace.data_ptr(), size, _stream(device))
     if rc:
         raise TQ4Error(rc, "moe_int8")

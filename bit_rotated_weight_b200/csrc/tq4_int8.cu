@@ -60,7 +60,7 @@ __device__ __forceinline__ void take_rows(const RowsArgs& a, int64_t row, int la
     if (e >= 0 && e < a.num_experts) {
       at = atomicAdd(a.cursor + e, 1);
       a.pairs[at] = static_cast<int32_t>(slot);
-      a.row_w[at] = __ldg(a.topk_w + slot);
+      a.row_w[at] = a.topk_w[slot];
     }
     s_at[j] = at;
   }
@@ -183,11 +183,11 @@ constexpr int kDeqGroups = 4;   // groups of 4 codes per thread
 // Back to fp32.  Bound by DRAM: 14336 x 4096 in 43 us, 6.8 TB/s (the codes
 // come from L2 in part).
 
-__global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* __restrict__ q,
-                                                              const float* __restrict__ scale,
-                                                              float* __restrict__ out, int64_t rows, int32_t kg) {
+__global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* q, const float* scale, float* out,
+                                                              int64_t rows, int32_t kg) {
   // kg: groups of 4 codes in a row.  The block's first group is located with
   // one 64-bit division, the others from there.
+  pdl_wait();
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 * kDeqGroups);
   const int64_t row0 = first / kg, total = rows * kg;
   const uint32_t col0 = static_cast<uint32_t>(first - row0 * kg);
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* __re
     const uint32_t at = threadIdx.x + 256 * j;
     if (first + at >= total) break;
     c[j] = __ldcs(reinterpret_cast<const char4*>(q) + first + at);
-    s[j] = __ldg(scale + row0 + (col0 + at) / static_cast<uint32_t>(kg));
+    s[j] = scale[row0 + (col0 + at) / static_cast<uint32_t>(kg)];
   }
 #pragma unroll
   for (int j = 0; j < kDeqGroups; ++j) {
@@ -215,9 +215,8 @@ __global__ void __launch_bounds__(256) int8_dequantize_kernel(const int8_t* __re
 // the first is added.  Bound by DRAM: 4096 tokens x 6 slots of 2688 in 43 us,
 // 6.6 TB/s.
 template <typename T>
-__global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restrict__ z, const int32_t* __restrict__ ids,
-                                                           int64_t m, int32_t topk, int32_t hg, int32_t num_experts,
-                                                           T* __restrict__ y) {
+__global__ void __launch_bounds__(256) int8_combine_kernel(const float* z, const int32_t* ids, int64_t m, int32_t topk,
+                                                           int32_t hg, int32_t num_experts, T* y) {
   pdl_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= m * hg) return;
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restri
       e[j] = -1;
       if (j0 + j < topk) {
         v[j] = __ldcs(zt + static_cast<int64_t>(j0 + j) * hg);
-        e[j] = __ldg(idt + j0 + j);
+        e[j] = __ldcg(idt + j0 + j);
       }
     }
 #pragma unroll
@@ -262,24 +261,23 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* __restri
 // one expert), their number, the number of rows, and each expert's first row
 // (the scatter's cursors).  With `pairs` the rows are given out here: the slot
 // and weight of each sorted row.  One block: the slots are few bytes.
-__global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* __restrict__ ids, int64_t slots,
-                                                             int32_t num_experts, int32_t chunk,
-                                                             int32_t* __restrict__ cursor, int4* __restrict__ segs,
-                                                             int32_t* __restrict__ nseg, int32_t* __restrict__ nrows,
-                                                             const float* __restrict__ topk_w,
-                                                             int32_t* __restrict__ pairs, float* __restrict__ row_w) {
+__global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* ids, int64_t slots, int32_t num_experts,
+                                                             int32_t chunk, int32_t* cursor, int4* segs, int32_t* nseg,
+                                                             int32_t* nrows, const float* topk_w, int32_t* pairs,
+                                                             float* row_w) {
   extern __shared__ int32_t count[];
   __shared__ int32_t s_rows[32], s_segs[32];
   __shared__ int32_t s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
+  pdl_wait();
   for (int e = tid; e < num_experts; e += 1024) count[e] = 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
   for (int64_t p0 = tid; p0 < slots; p0 += 8 * 1024) {   // (eight loads in flight a thread)
     int32_t e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = p0 + j * 1024 < slots ? __ldg(ids + p0 + j * 1024) : INT32_MIN;
+    for (int j = 0; j < 8; ++j) e[j] = p0 + j * 1024 < slots ? __ldcg(ids + p0 + j * 1024) : INT32_MIN;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (e[j] >= 0 && e[j] < num_experts) atomicAdd(&count[e[j]], 1);
@@ -368,17 +366,27 @@ cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
   return cudaLaunchKernelEx(&cfg, int8_rows_any_kernel<T>, a);
 }
 
-// `dependent`: may be set up while the kernel before it still runs (it waits
-// for its end before its first load).
-cudaError_t launch_rows(int dtype, const RowsArgs& a, bool dependent, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kRowThreads);
+// A launch that may be set up while the kernel before it still runs (every
+// kernel here waits for its end before its first load or store, and reads by
+// plain loads: read-only ones are for what nothing writes while a kernel runs).
+// A plain launch costs the host a microsecond more.
+void launch_early(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, unsigned grid, unsigned threads, size_t smem,
+                  cudaStream_t st) {
+  cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 1 : 0;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+}
+
+cudaError_t launch_rows(int dtype, const RowsArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  launch_early(cfg, attr, 1, kRowThreads, 0, st);   // (the grid is set below)
   const cudaError_t e = dtype == TQ_DTYPE_F32    ? launch_rows_of<float>(a, cfg)
                         : dtype == TQ_DTYPE_BF16 ? launch_rows_of<__nv_bfloat16>(a, cfg)
                                                  : launch_rows_of<__half>(a, cfg);
@@ -477,12 +485,17 @@ MoeLayout moe_layout(int64_t m, int32_t topk, int64_t experts, int64_t H, int64_
   L.slots = m * topk;
   // Rows of a segment, by the mean rows of an expert.  While the weight's
   // stream bounds the layer the width hardly matters (128 experts, 512 tokens
-  // x 6: 237 us at 64 and 128, 243 at 32, 261 at 256); below one row it is the
-  // launches, and the form without quantizing kernels is shorter (1 token 22.7
-  // us, against 25.2); from 136 on it is the MMAs (4096 tokens: 456 us at 256,
-  // 507 at 128; 2048: 351 and 321).
+  // x 6: 237 us at 64 and 128, 243 at 32, 261 at 256); from 136 on it is the MMAs
+  // (4096 tokens: 456 us at 256, 507 at 128; 2048: 351 and 321).
+  // Of few rows it is the launches, and the form without quantizing kernels
+  // (16) is shorter, three launches against six: 16 x 8 slots of 128 experts of
+  // 2688 x 1856 138 us and 143, of 1088 x 896 39 and 49; 32 slots of 4 experts of
+  // 512 x 512 14 and 16.5.  But there every CTA quantizes its experts' rows
+  // itself, which pays up to about 16384 values an expert: 111 slots of 30
+  // experts of 2688 x 1856 (16800) 76 us and 68, 64 of 4 (72700) 34 and 24.
   const int64_t mean = L.slots / experts;
-  L.nt = mean < 1 ? 16 : mean < 40 ? 64 : mean < 136 ? 128 : 256;
+  const bool few = L.slots <= kStreamSlots && L.slots * (H + I) <= 16384 * experts;
+  L.nt = mean < 1 || few ? 16 : mean < 40 ? 64 : mean < 136 ? 128 : 256;
   L.maxseg = L.slots / L.nt + (experts < L.slots ? experts : L.slots);
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -535,7 +548,7 @@ TQ_API int tq4_1s_int8_quantize(const void* W, int dtype, const tq4_1s_int8_weig
   a.rows = rows;
   a.q = out->q;
   a.scale = out->wscale;
-  return rc_of(launch_rows(dtype, a, false, reinterpret_cast<cudaStream_t>(stream)));
+  return rc_of(launch_rows(dtype, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4_stream_t stream) {
@@ -548,8 +561,12 @@ TQ_API int tq4_1s_int8_dequantize(const tq4_1s_int8_weight* w, float* W_out, tq4
   const int64_t rows = w->n * w->num_experts, kg = w->k / 4;
   const int64_t blocks = (rows * kg + 256 * kDeqGroups - 1) / (256 * kDeqGroups);
   if (blocks > INT32_MAX) return TQ_ERR_INVALID_ARG;
-  int8_dequantize_kernel<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      w->q, w->wscale, W_out, rows, static_cast<int32_t>(kg));
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  launch_early(cfg, attr, static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, int8_dequantize_kernel, static_cast<const int8_t*>(w->q),
+                                           static_cast<const float*>(w->wscale), W_out, rows, static_cast<int32_t>(kg));
+  if (e != cudaSuccess) return TQ_ERR_CUDA;
   note_launches(1);
   return rc_of(cudaGetLastError());
 }
@@ -613,7 +630,7 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   r.rows = m;
   r.q = xq;
   r.scale = reinterpret_cast<float*>(base + L.xscale);
-  if (launch_rows(dtype, r, false, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(w->n);
   a.m = static_cast<int32_t>(m);
@@ -661,21 +678,23 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
   int8_t* hq = reinterpret_cast<int8_t*>(base + L.hq);
   int4* segs = reinterpret_cast<int4*>(base + L.segs);
-  alignas(64) CUtensorMap tu, tx, td, th;
-  if (!encode_i8_map(&tu, up->q, E, I, H, 128) || !encode_i8_map(&tx, xq, 0, L.slots, H, L.nt) ||
-      !encode_i8_map(&td, down->q, E, H, I, 128) || !encode_i8_map(&th, hq, 0, L.slots, I, L.nt))
-    return TQ_ERR_CUDA;
-
   // few rows an expert: the products quantize their rows themselves
   const bool stream_rows = L.nt == kStreamTokens && int8_stream_fits(H) && int8_stream_fits(I);
+  alignas(64) CUtensorMap tu, tx, td, th;
+  if (!encode_i8_map(&tu, up->q, E, I, H, 128) || !encode_i8_map(&td, down->q, E, H, I, 128)) return TQ_ERR_CUDA;
+  if (!stream_rows && (!encode_i8_map(&tx, xq, 0, L.slots, H, L.nt) || !encode_i8_map(&th, hq, 0, L.slots, I, L.nt)))
+    return TQ_ERR_CUDA;
   // and where the slots fit a block's routing they need no kernel for that
   const bool routed = stream_rows && L.slots <= kStreamSlots;
   if (!routed) {
-    int8_segments_kernel<<<1, 1024, static_cast<size_t>(E) * 4, st>>>(
-        topk_ids, L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
-        stream_rows ? i32(L.pairs) : nullptr, f32(L.row_w));
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    launch_early(cfg, attr, 1, 1024, static_cast<size_t>(E) * 4, st);
+    if (cudaLaunchKernelEx(&cfg, int8_segments_kernel, topk_ids, L.slots, static_cast<int32_t>(E),
+                           static_cast<int32_t>(L.nt), i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
+                           stream_rows ? i32(L.pairs) : static_cast<int32_t*>(nullptr), f32(L.row_w)) != cudaSuccess)
+      return TQ_ERR_CUDA;
     note_launches(1);
-    if (cudaGetLastError() != cudaSuccess) return TQ_ERR_CUDA;
   }
   const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
   if (stream_rows) {
@@ -727,7 +746,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   r.pairs = i32(L.pairs);
   r.topk_w = topk_w;
   r.row_w = f32(L.row_w);
-  if (launch_rows(dtype, r, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
   a.n = static_cast<int32_t>(I);
   a.row_tiles = static_cast<int32_t>(rt_up);
@@ -747,7 +766,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   g.q = hq;
   g.scale = f32(L.hscale);
   g.rows_dev = i32(L.nrows);
-  if (launch_rows(TQ_DTYPE_BF16, g, true, st) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_rows(TQ_DTYPE_BF16, g, st) != cudaSuccess) return TQ_ERR_CUDA;
   a.n = static_cast<int32_t>(H);
   a.row_tiles = static_cast<int32_t>(rt_dn);
   a.ksteps = static_cast<int32_t>((I + 127) / 128);
@@ -762,15 +781,9 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   }
   const int32_t hg = static_cast<int32_t>(H / 4), experts = static_cast<int32_t>(E);
   const unsigned blocks = static_cast<unsigned>((m * hg + 255) / 256);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  launch_early(cfg, attr, blocks, 256, 0, st);
   const float* z = f32(L.z);
   const cudaError_t e =
       dtype == TQ_DTYPE_BF16

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
       tc_fence_after();
       const int row = pl.row0 + t;
       const uint32_t d_addr = tmem + lane_base + db * NT;
-      const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
+      const float sw = row < a.n ? __ldcg(a.wscale + static_cast<int64_t>(pl.expert) * a.n + row) : 0.0f;
       finish_columns<NT>(a, pl, row, sw, d_addr, col0, kCols, sh.sx[db], sh.tw[db], sh.slot[db]);
       tc_fence_before();
       mbar_arrive(&sh.dempty[db]);
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (!sh.epi_ok[db]) break;
       tc_fence_after();
       const int row = pl.row0 + t;
-      const float sw = row < a.n ? __ldg(a.wscale + row) : 0.0f;
+      const float sw = row < a.n ? __ldcg(a.wscale + row) : 0.0f;
       finish_columns<kPairTok>(a, pl, row, sw, tmem + lane_base + db * kPairTok, col0, kPairTok / 2, sh.sx[db],
                                nullptr, nullptr);
       tc_fence_before();

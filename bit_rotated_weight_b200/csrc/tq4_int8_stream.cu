@@ -25,8 +25,8 @@
 // their int32 sums by asynchronous stores into each other's shared memory that
 // the receiver counts in bytes: no workspace, no second kernel.
 // Grouped, with at most 128 slots, every CTA sorts the slots by expert itself
-// (a count of smaller ids per slot): a kernel for that took 3 us of a token's
-// 24, and its results came three memory latencies later.  The down projection
+// (a count of smaller ids per slot, 0.5 to 1 us): a kernel for that took 3 us of
+// a token's 24, and its results came three memory latencies later.  The down projection
 // does so, and starts its weight copies, before it waits for the up projection.
 // Role loops are not unrolled: a call of a few microseconds runs most of the
 // code once, and fetching instructions was most of its time.
@@ -72,51 +72,63 @@ struct Shared {
   // routing in the kernel
   int32_t nseg;
   alignas(16) int32_t id[kStreamSlots];
-  int32_t sub[kStreamSlots];               // segments of a slot's expert, at its first slot
+  alignas(16) int32_t sub[kStreamSlots];   // segments of a slot's expert, at its first slot
   int4 segs[kStreamSlots];
   int32_t pairs[kStreamSlots];
   float row_w[kStreamSlots];
 };
 
 // Sorts the slots by expert, by the whole block: a slot's row is the number of
-// slots with a smaller id, or the same id earlier.  Ids out of range are left
-// out.  (The ids are ready before this call's first kernel.)
+// slots with a smaller id, or the same id earlier.  Four threads count for a
+// slot (one each took 10 us of a layer with 128 slots).  Ids out of range are
+// left out.  (The ids are ready before this call's first kernel.)
 __device__ __forceinline__ void route(Shared& sh, const Int8StreamArgs& a) {
-  const int t = threadIdx.x;
-  if (t == 0) sh.nseg = 0;
+  static_assert(kThreads == 4 * kStreamSlots, "four threads a slot");
+  const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
+  if (threadIdx.x == 0) sh.nseg = 0;
   int32_t id = INT32_MAX;
   float w = 0.0f;
-  if (t < kStreamSlots) {
-    if (t < a.slots) {
-      id = __ldcg(a.ids + t);
-      w = __ldcg(a.topk_w + t);
-      if (id < 0 || id >= a.experts) {
-        if (blockIdx.x == 0) raise_status(TQ_DEV_BAD_ROUTING);
-        id = INT32_MAX;
-      }
+  if (t < a.slots) {
+    id = __ldcg(a.ids + t);
+    w = __ldcg(a.topk_w + t);
+    if (id < 0 || id >= a.experts) {
+      if (blockIdx.x == 0 && part == 0) raise_status(TQ_DEV_BAD_ROUTING);
+      id = INT32_MAX;
     }
+  }
+  if (part == 0) {
     sh.id[t] = id;
     sh.sub[t] = 0;
   }
   __syncthreads();
+  auto all = [](int v) {
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+    return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+  };
   int less = 0, same = 0, before = 0;
-  if (id != INT32_MAX) {
 #pragma unroll 1
-    for (int q = 0; q < a.slots; q += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(&sh.id[q]);
-      less += (o.x < id) + (o.y < id) + (o.z < id) + (o.w < id);
-      same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
-      before += (o.x == id && q < t) + (o.y == id && q + 1 < t) + (o.z == id && q + 2 < t) + (o.w == id && q + 3 < t);
-    }
+  for (int q = 4 * part; q < a.slots; q += 16) {
+    const int4 o = *reinterpret_cast<const int4*>(&sh.id[q]);
+    less += (o.x < id) + (o.y < id) + (o.z < id) + (o.w < id);
+    same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+    before += (o.x == id && q < t) + (o.y == id && q + 1 < t) + (o.z == id && q + 2 < t) + (o.w == id && q + 3 < t);
+  }
+  less = all(less), same = all(same), before = all(before);
+  const bool valid = id != INT32_MAX;
+  if (valid && part == 0) {
     sh.pairs[less + before] = t;
     sh.row_w[less + before] = w;
     if (before == 0) sh.sub[t] = (same + kTok - 1) / kTok;
   }
   __syncthreads();
-  if (id != INT32_MAX && before == 0) {
-    int at = 0;
+  int at = 0;   // segments of smaller ids
 #pragma unroll 1
-    for (int q = 0; q < a.slots; ++q) at += sh.id[q] < id ? sh.sub[q] : 0;
+  for (int q = 4 * part; q < a.slots; q += 16) {
+    const int4 o = *reinterpret_cast<const int4*>(&sh.id[q]), n = *reinterpret_cast<const int4*>(&sh.sub[q]);
+    at += (o.x < id ? n.x : 0) + (o.y < id ? n.y : 0) + (o.z < id ? n.z : 0) + (o.w < id ? n.w : 0);
+  }
+  at = all(at);
+  if (valid && before == 0 && part == 0) {
     for (int i = 0; i < same; i += kTok) sh.segs[at++] = make_int4(id, less + i, min(kTok, same - i), 0);
     atomicAdd(&sh.nseg, (same + kTok - 1) / kTok);
   }
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fresh = false;
       }
       const int row = w.row_tile * kRows + t;
-      const float sw = row < a.n ? __ldg(a.wscale + static_cast<int64_t>(sg.x) * a.n + row) : 0.0f;
+      const float sw = row < a.n ? __ldcg(a.wscale + static_cast<int64_t>(sg.x) * a.n + row) : 0.0f;
       ok = ok && mbar_wait(&sh.dfull[db], (ti >> 1) & 1, abortp);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok && !CLUSTER) break;
@@ -523,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int4 v = *reinterpret_cast<const int4*>(&sh.part[(p * per + rl) * kPartRow + j0]);
             sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
           }
-          const float osw = __ldg(a.wscale + out_row);
+          const float osw = __ldcg(a.wscale + out_row);
           const int32_t v[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)

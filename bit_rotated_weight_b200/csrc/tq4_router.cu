@@ -31,9 +31,11 @@ struct RouterArgs {
   float scale;
 };
 
-__device__ __forceinline__ float load_logit(const float* z) { return __ldg(z); }
+// (Plain loads: the kernel before may still write the logits and the biases
+// when this one starts, which read-only loads do not allow.)
+__device__ __forceinline__ float load_logit(const float* z) { return *z; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* z) {
-  return bf16_bits_to_f32(__ldg(reinterpret_cast<const uint16_t*>(z)));
+  return bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(z));
 }
 
 __device__ __forceinline__ double warp_max(double v) {
@@ -99,7 +101,7 @@ __device__ __noinline__ void slow_row(const RouterArgs& a, int64_t t, double* ch
     double c = -kInf;
     if ((open >> i) & 1u) {
       if (a.bias) {
-        const float b = __ldg(a.bias + e);
+        const float b = a.bias[e];
         if (b < INFINITY) {
           c = score(e) + static_cast<double>(b);
         } else {   // NaN or +inf
@@ -360,7 +362,7 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
   int id = from + 32 * (PL - 1 - (taken & (PL - 1)));
   float z = got ? load_logit(zt + id) : 0.0f;
   {
-    const float b = got && BIASED ? __ldg(a.bias + id) : 0.0f;
+    const float b = got && BIASED ? a.bias[id] : 0.0f;
     const float mine = value_of(taken & ~(PL - 1)), next = __shfl_down_sync(kAll, mine, 1);
     const int32_t next_key = __shfl_down_sync(kAll, taken, 1);
     auto room = [&](float x, float y) {
@@ -432,7 +434,7 @@ __device__ __forceinline__ void lane_of(const RouterArgs& a, bool biased, Lane<P
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = lane + 32 * i;
-    l.bias[i] = biased && e < a.experts ? __ldg(a.bias + e) : 0.0f;
+    l.bias[i] = biased && e < a.experts ? a.bias[e] : 0.0f;
     plain = plain && fabsf(l.bias[i]) < INFINITY;
     if (a.keep < a.groups && e < a.experts) l.group[i >> 2] |= static_cast<uint32_t>(e / l.size) << (8 * (i & 3));
   }
@@ -572,6 +574,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   uint4* tile = reinterpret_cast<uint4*>(mine);
   float* s_rank = reinterpret_cast<float*>(mine + kRowsOf * sh.stride * 16) + own;   // [group][token]
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRowsWarps + warp) * kRowsOf;
+  pdl_wait();
   const int rows = static_cast<int>(a.m - t0 < kRowsOf ? (a.m > t0 ? a.m - t0 : 0) : kRowsOf);
   {
     const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + t0 * a.experts);
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   bool plain = true;
   if (BIASED)
     for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
-      const float b = __ldg(a.bias + e);
+      const float b = a.bias[e];
       s_bias[e + 4 * static_cast<int>((e + 0.5f) * sh.per_size)] = b;   // (e / size)
       plain = plain && fabsf(b) <= 2.5f;   // (for the keys' range: 1 + 3 may round to 4; NaN and infinities too)
     }
@@ -898,6 +901,7 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 8 : PL == 16 ? 6 : 4)
   constexpr int kSpace = PL * 64 > PL * 32 + 1024 ? PL * 64 : PL * 32 + 1024;
   __shared__ alignas(8) float s_space[kWarps][kSpace];
   const int warp = threadIdx.x >> 5;
+  pdl_wait();
   Lane<PL> l;
   lane_of<T, PL>(a, BIASED, l);
   // topk + 1 keys are taken, one per lane
@@ -909,18 +913,36 @@ __global__ void __launch_bounds__(kWarps * 32, PL <= 8 ? 8 : PL == 16 ? 6 : 4)
     }
 }
 
+// A launch that may be set up while the kernel before it still runs (the
+// kernels wait for its end first).  A plain launch of one row costs the host a
+// microsecond more (4.8 and 3.6 us a call), and the GPU 0.2.
+void launch_early(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, unsigned grid, unsigned threads, size_t smem,
+                  cudaStream_t st) {
+  cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+}
+
 template <typename T, int PL>
 cudaError_t launch_as(const RouterArgs& a, cudaStream_t st) {
   // a few rows a warp: each loads the biases once
   const int64_t blocks = (a.m + kWarps - 1) / kWarps, most = 148 * 8 * 2;
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (a.sigmoid) {
-    if (a.bias) router_scored_kernel<T, PL, true, true><<<grid, kWarps * 32, 0, st>>>(a);
-    else router_scored_kernel<T, PL, true, false><<<grid, kWarps * 32, 0, st>>>(a);
-  } else {
-    if (a.bias) router_scored_kernel<T, PL, false, true><<<grid, kWarps * 32, 0, st>>>(a);
-    else router_scored_kernel<T, PL, false, false><<<grid, kWarps * 32, 0, st>>>(a);
-  }
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  launch_early(cfg, attr, grid, kWarps * 32, 0, st);
+  const cudaError_t e =
+      a.sigmoid ? (a.bias ? cudaLaunchKernelEx(&cfg, router_scored_kernel<T, PL, true, true>, a)
+                          : cudaLaunchKernelEx(&cfg, router_scored_kernel<T, PL, true, false>, a))
+                : (a.bias ? cudaLaunchKernelEx(&cfg, router_scored_kernel<T, PL, false, true>, a)
+                          : cudaLaunchKernelEx(&cfg, router_scored_kernel<T, PL, false, false>, a));
+  if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
 }
@@ -940,8 +962,12 @@ cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const RowsShape s = rows_shape<T>(a);
   const int64_t rows = kRowsOf * kRowsWarps;
-  router_rows_kernel<T, SIGMOID, BIASED><<<static_cast<unsigned>((a.m + rows - 1) / rows), kRowsWarps * 32,
-                                           s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st>>>(a, s);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  launch_early(cfg, attr, static_cast<unsigned>((a.m + rows - 1) / rows), kRowsWarps * 32,
+               s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, router_rows_kernel<T, SIGMOID, BIASED>, a, s);
+  if (r != cudaSuccess) return r;
   note_launches(1);
   return cudaGetLastError();
 }
