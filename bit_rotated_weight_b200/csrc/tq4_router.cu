@@ -212,11 +212,27 @@ __device__ __noinline__ double exact_score(double x, bool sigmoid) {
   const double e = exp(sigmoid ? -x : x);
   return sigmoid ? 1.0 / (1.0 + e) : e;
 }
-// An expert's choice value in fp64 (softmax's with a bias would need its sum;
-// not here).
-template <bool BIASED>
-__device__ __forceinline__ double exact_choice(float z, float b) {
-  return BIASED ? exact_score(static_cast<double>(z), true) + static_cast<double>(b) : static_cast<double>(z);
+// 1 / sum exp(z - top) in fp64 from the fp32 sum of 2^(z log2(e) - top2): without
+// the rounding of top2, which all of the sum's terms share.
+__device__ __forceinline__ double exact_inv(float top, float top2, float inv) {
+  const double shared = static_cast<double>(top) * static_cast<double>(kLog2e) - static_cast<double>(top2);
+  return static_cast<double>(inv) * (1.0 + 0.6931471805599453 * shared);
+}
+// An expert's choice value in fp64, and the part of it that the fp32 sum of
+// softmax leaves uncertain: of two values that are near, the error is that of
+// the difference of their parts.
+struct Choice {
+  double value, part;
+};
+template <bool SIGMOID, bool BIASED>
+__device__ __forceinline__ Choice exact_choice(float z, float b, float top, double inv) {
+  if (!BIASED) return {static_cast<double>(z), 0.0};
+  if (SIGMOID) return {exact_score(static_cast<double>(z), true) + static_cast<double>(b), 0.0};
+  const double s = exact_score(static_cast<double>(z) - static_cast<double>(top), false) * inv;
+  return {s + static_cast<double>(b), s};
+}
+__device__ __forceinline__ bool unclear(const Choice& a, const Choice& b, float rel) {
+  return a.part != b.part && fabs(a.value - b.value) <= static_cast<double>(rel) * fabs(a.part - b.part);
 }
 
 // What a warp keeps from row to row.
@@ -241,14 +257,15 @@ struct Lane {
 //   Errors of a value c = s + b against fp64.  Sigmoid: rcp.approx 2^-23 s,
 //   the add of 1 2^-24 s, and through s (1 - s) <= 1/4 ex2.approx's 2^-22 and
 //   the exponent's roundings, |z| 2^-23 (s (1 - s) |z| <= 0.224): under 3e-7.
-//   Softmax has the sum's roundings too,
-//   PL + 5 adds: under (PL + 16) 2^-24.  The bias' add: 2^-24 |c|; the key's
-//   lowest bits: PL 2^-23 |c|.
-// Without a bias the keys are the logits' own, and only the lowest bits go.
+//   Softmax has the sum's roundings too, in units of 2^-24 of the largest score
+//   (1 / sum): PL + 5 adds, ex2's 4, its arguments' (the mean of |arg| under
+//   weights 2^arg is at most log2 E, so 7) and log2(e)'s 2, rcp's 2: PL + 24.
+//   The bias' add: 2^-24 |c|; the key's lowest bits: PL 2^-23 |c|.
+// Without a bias the keys are the logits' own, and only the lowest bits go (a
+// bf16 logit's are zeros: nothing is lost, and equal ones are in order).
 template <typename T, int PL, bool SIGMOID, bool BIASED>
 __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const Lane<PL>& l, float* s_value) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  constexpr float kErr = SIGMOID ? 3e-7f : (PL + 16) * 0x1p-24f;
   const int lane = threadIdx.x & 31;
   const T* zt = static_cast<const T*>(a.logits) + t * a.experts;
   const bool grouped = a.keep < a.groups;
@@ -260,12 +277,12 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
   for (int i = 0; i < PL; ++i) near_zero = near_zero && fabsf(v[i]) < 40.0f;   // (not of a NaN)
   // beyond 40 an fp32 weight may underflow where its fp64 form does not
   if (!__all_sync(kAll, near_zero)) return false;
-  float top2 = 0.0f, sum = 1.0f;   // softmax: log2(e) times the largest logit
+  float top = -INFINITY, top2 = 0.0f, sum = 1.0f;   // softmax: the largest logit, times log2(e)
   if (!SIGMOID) {
-    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PL; ++i) top = fmaxf(top, lane + 32 * i < a.experts ? v[i] : -INFINITY);
-    top2 = value_of(__reduce_max_sync(kAll, key_of(top))) * kLog2e;
+    top = value_of(__reduce_max_sync(kAll, key_of(top)));
+    top2 = top * kLog2e;
     if (BIASED || !a.renorm || (grouped && a.top2)) {
       sum = 0.0f;
 #pragma unroll
@@ -275,6 +292,8 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
     }
   }
   const float inv = rcp(sum);
+  constexpr float kRel = (PL + 24) * 0x1p-24f;
+  const float err = SIGMOID ? 3e-7f : kRel * inv;
   auto score = [&](float z) { return SIGMOID ? rcp(1.0f + ex2(z * -kLog2e)) : ex2(fmaf(z, kLog2e, -top2)) * inv; };
   if (BIASED) {
 #pragma unroll
@@ -319,7 +338,7 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
     if (BIASED || a.top2) {
       const float in = value_of(last), out = value_of(__reduce_max_sync(kAll, key));
       // two values in each rank, and the rounding of their sums
-      if (in - out <= 4.0f * kErr + 0x1p-21f * fmaxf(fabsf(in), fabsf(out))) return false;
+      if (in - out <= 4.0f * err + 0x1p-21f * fmaxf(fabsf(in), fabsf(out))) return false;
     }
     __syncwarp();   // (the next row writes s_value again)
   }
@@ -361,12 +380,12 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
   const bool got = lane <= a.topk && taken != kNone;
   int id = from + 32 * (PL - 1 - (taken & (PL - 1)));
   float z = got ? load_logit(zt + id) : 0.0f;
-  {
+  if constexpr (BIASED || sizeof(T) == 4) {
     const float b = got && BIASED ? a.bias[id] : 0.0f;
     const float mine = value_of(taken & ~(PL - 1)), next = __shfl_down_sync(kAll, mine, 1);
     const int32_t next_key = __shfl_down_sync(kAll, taken, 1);
     auto room = [&](float x, float y) {
-      return BIASED ? 2.0f * kErr + fmaxf(fabsf(x), fabsf(y)) * ((PL + 2) * 0x1p-23f) : 0.0f;
+      return BIASED ? 2.0f * err + fmaxf(fabsf(x), fabsf(y)) * ((PL + 2) * 0x1p-23f) : 0.0f;
     };
     bool near = lane < a.topk && next_key != kNone && mine - next <= room(mine, next);
     const bool last = (__ballot_sync(kAll, near) >> (a.topk - 1)) & 1u;
@@ -381,16 +400,18 @@ __device__ __forceinline__ bool fast_row(const RouterArgs& a, int64_t t, const L
     }
     const uint32_t nears = __ballot_sync(kAll, near);
     if (nears) {   // the keys taken are ranked again by their values in fp64
-      if (!SIGMOID && BIASED) return false;
-      const double c = got ? exact_choice<BIASED>(z, b) : 0.0;
+      const Choice c = got ? exact_choice<SIGMOID, BIASED>(z, b, top, exact_inv(top, top2, inv)) : Choice{0.0, 0.0};
       const int n = a.topk + (last ? 1 : 0);
       int place = 0;
+      bool open = false;
       for (int o = 0; o < n; ++o) {
-        const double oc = __shfl_sync(kAll, c, o);
+        const Choice oc = {__shfl_sync(kAll, c.value, o), SIGMOID || !BIASED ? 0.0 : __shfl_sync(kAll, c.part, o)};
         const int oid = __shfl_sync(kAll, id, o);
         const bool is = __shfl_sync(kAll, static_cast<int>(got), o) != 0;
-        place += is && (oc > c || (oc == c && oid < id)) ? 1 : 0;
+        place += is && (oc.value > c.value || (oc.value == c.value && oid < id)) ? 1 : 0;
+        open = open || (got && lane < n && is && unclear(oc, c, kRel));
       }
+      if (!SIGMOID && BIASED && __any_sync(kAll, open)) return false;
       if (!got || lane >= n) place = lane;
       int new_id = id;
       float new_z = z;
@@ -470,13 +491,15 @@ __device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plai
 // 2^-20 (of the float's 32 bits those above are the same for all).  A float's
 // own bits, cut to make room for the expert, would count 2^-15 near 1, and
 // 1.5 % of the rows would be near ties; so it is 0.1 %.  Two neighbours that
-// are near are told apart in fp64 in place; what is left (three that are near,
-// groups that are, softmax with a bias) is done again by the whole warp, which
-// costs little work but 10 us of fetching code that is otherwise not run.
+// are near are told apart in fp64 in place, and so are two groups; what is left
+// (three that are near) is done again by the whole warp, which costs little
+// work but 10 us of fetching code that is otherwise not run.  (27447 x 148,
+// softmax with a bias: 11.7 us; 24.6 with its near pairs left to the warp, 43
+// by a warp a row.)
 constexpr int kRowsWarps = 2;
 constexpr int kRowsTopk = 8;
 constexpr int kRowsOf = 8;         // tokens of a warp
-constexpr int kRowsBytes = 1024;   // largest row
+constexpr int kRowsPlaces = 512;   // nine bits
 constexpr int kRowsLeast = 256;
 
 __device__ __forceinline__ void order2(int32_t& a, int32_t& b) {
@@ -539,26 +562,35 @@ __device__ __forceinline__ void eight(const __nv_bfloat16* z, float (&v)[8]) {
 __device__ __forceinline__ float in_shared(const float* z) { return *z; }
 __device__ __forceinline__ float in_shared(const __nv_bfloat16* z) { return __bfloat162float(*z); }
 
+// In shared memory a group has places for `wide` experts, a multiple of eight;
+// those behind its `size` hold a value that is never chosen.
+constexpr float kPad = -128.0f, kPadBias = -3.9f;   // (score 0; below any bias of a row done here)
 struct RowsShape {
   int pieces, stride;   // 16-byte pieces of a row, and from row to row in shared memory
-  int size, bits, mask; // experts of a group; the key bits that hold the expert
-  float per_size;       // 1 / size
+  int size, wide;       // experts of a group, and its places
+  int bits, mask;       // the key bits that hold the place
+  float per_size, per_wide;   // 1 / size, 1 / wide
+  int whole;            // rows can be copied in pieces: no padding, on 16-byte boundaries
   int bias_floats, warp_bytes;
 };
 template <typename T>
 RowsShape rows_shape(const RouterArgs& a) {
   RowsShape s;
-  s.pieces = a.experts * static_cast<int>(sizeof(T)) / 16;
-  s.stride = s.pieces | 1;
   s.size = a.experts / a.groups;
+  s.wide = (s.size + 7) & ~7;
+  const int places = s.wide * a.groups;
+  s.pieces = places * static_cast<int>(sizeof(T)) / 16;
+  s.stride = s.pieces | 1;
   s.per_size = 1.0f / static_cast<float>(s.size);
+  s.per_wide = 1.0f / static_cast<float>(s.wide);
+  s.whole = s.size == s.wide && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 ? 1 : 0;
   s.bits = 0;
-  while ((1 << s.bits) < a.experts) ++s.bits;
+  while ((1 << s.bits) < places) ++s.bits;
   s.mask = (1 << s.bits) - 1;
   // groups' biases lie 4 floats further apart, so that threads at different groups read different banks
-  s.bias_floats = a.bias ? a.experts + 4 * a.groups : 0;
+  s.bias_floats = a.bias ? places + 4 * a.groups : 0;
   // the rows and their groups' ranks; then, in the same place, what again_row needs
-  const int rows = kRowsOf * (s.stride * 16 + a.groups * 4), again = a.experts * 8 + 4096;
+  const int rows = kRowsOf * (s.stride * 16 + a.groups * 4), again = (a.experts * 8 + 4096 + 15) & ~15;
   s.warp_bytes = rows > again ? rows : again;
   return s;
 }
@@ -576,26 +608,51 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRowsWarps + warp) * kRowsOf;
   pdl_wait();
   const int rows = static_cast<int>(a.m - t0 < kRowsOf ? (a.m > t0 ? a.m - t0 : 0) : kRowsOf);
-  {
-    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + t0 * a.experts);
+  auto div_size = [&](int e) { return static_cast<int>((e + 0.5f) * sh.per_size); };   // (exact: e < 512)
+  auto div_wide = [&](int e) { return static_cast<int>((e + 0.5f) * sh.per_wide); };
+  const int extra = sh.wide - sh.size;
+  const T* from = static_cast<const T*>(a.logits) + t0 * a.experts;
+  if (sh.whole) {
     int row = 0, at = lane;
     while (at >= sh.pieces) at -= sh.pieces, ++row;
 #pragma unroll 4
     for (int i = lane; i < rows * sh.pieces; i += 32) {
       const uint32_t to = smem_u32(tile + row * sh.stride + at);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from + i) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(reinterpret_cast<const uint4*>(from) + i)
+                   : "memory");
       at += 32;
       while (at >= sh.pieces) at -= sh.pieces, ++row;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  } else if (rows > 0) {
+    T* const to = reinterpret_cast<T*>(tile);
+    const int step = sh.stride * (16 / static_cast<int>(sizeof(T)));
+#pragma unroll 2
+    for (int e = lane; e < a.experts; e += 32) {
+      T v[kRowsOf];
+#pragma unroll
+      for (int r = 0; r < kRowsOf; ++r) v[r] = from[(r < rows ? r : 0) * a.experts + e];
+      const int at = e + div_size(e) * extra;
+#pragma unroll
+      for (int r = 0; r < kRowsOf; ++r) to[r * step + at] = v[r];
+    }
+    for (int g = 0; g < a.groups; ++g)
+      for (int i = lane; i < extra * kRowsOf; i += 32)
+        to[(i & (kRowsOf - 1)) * step + g * sh.wide + sh.size + i / kRowsOf] = static_cast<T>(kPad);
   }
   bool plain = true;
-  if (BIASED)
+  if (BIASED) {
     for (int e = threadIdx.x; e < a.experts; e += kRowsWarps * 32) {
       const float b = a.bias[e];
-      s_bias[e + 4 * static_cast<int>((e + 0.5f) * sh.per_size)] = b;   // (e / size)
+      const int g = div_size(e);
+      s_bias[e + g * (extra + 4)] = b;
       plain = plain && fabsf(b) <= 2.5f;   // (for the keys' range: 1 + 3 may round to 4; NaN and infinities too)
     }
+    for (int i = threadIdx.x; i < a.groups * extra; i += kRowsWarps * 32) {
+      const int g = i / extra;
+      s_bias[g * (sh.wide + 4) + sh.size + (i - g * extra)] = kPadBias;
+    }
+  }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   plain = __syncthreads_and(plain);
   if (rows == 0) return;
@@ -604,7 +661,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   bool done = plain && own < rows;   // decided here
   float largest = -INFINITY, top2 = 0.0f, inv = 1.0f;   // (softmax)
   if (!SIGMOID) {
-    for (int e = 8 * sub; e < a.experts; e += 32) {
+    for (int e = 8 * sub; e < sh.wide * a.groups; e += 32) {
       float v[8];
       eight(z + e, v);
 #pragma unroll
@@ -615,7 +672,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
     top2 = largest * kLog2e;
     if (BIASED || !a.renorm || (grouped && a.top2)) {
       float sum[2] = {0.0f, 0.0f};
-      for (int e = 8 * sub; e < a.experts; e += 32) {
+      for (int e = 8 * sub; e < sh.wide * a.groups; e += 32) {
         float v[8];
         eight(z + e, v);
 #pragma unroll
@@ -626,8 +683,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
       inv = rcp(all + __shfl_xor_sync(kAll, all, 2));
     }
   }
-  // (a sum's chain is at most 64 + 3 adds, each relative 2^-24)
-  constexpr float kErr = SIGMOID ? 3e-7f : 80 * 0x1p-24f;
+  // (as fast_row's, with an eighth of the row and 3 adds in a sum's chain)
+  const float rel = (0.125f * static_cast<float>(a.experts) + 24.0f) * 0x1p-24f, err = SIGMOID ? 3e-7f : rel * inv;
   auto score = [&](float x) { return SIGMOID ? rcp(1.0f + ex2(x * -kLog2e)) : ex2(fmaf(x, kLog2e, -top2)) * inv; };
   uint32_t kept = 0;
   float squares = 0.0f;   // of the logits seen
@@ -637,14 +694,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
     const bool alone = a.groups % 4 == 0;
     for (int g = alone ? sub : 0; g < a.groups; g += alone ? 4 : 1) {
       float first = -INFINITY, second = -INFINITY;
-      for (int j = alone ? 0 : 8 * sub; j < sh.size; j += alone ? 8 : 32) {
+      for (int j = alone ? 0 : 8 * sub; j < sh.wide; j += alone ? 8 : 32) {
         float v[8];
-        eight(z + g * sh.size + j, v);
+        eight(z + g * sh.wide + j, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) squares = fmaf(v[i], v[i], squares);
         if (BIASED || a.top2) {
           float b[8];
-          if (BIASED) eight(s_bias + g * (sh.size + 4) + j, b);
+          if (BIASED) eight(s_bias + g * (sh.wide + 4) + j, b);
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = BIASED ? score(v[i]) + b[i] : score(v[i]);
         }
@@ -684,7 +741,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
     }
     if (BIASED || a.top2) {
       // two values' errors in each rank, and the rounding of their sums
-      const float room = 4.0f * kErr + 0x1p-21f * fmaxf(fabsf(in), fabsf(out));
+      const float room = 4.0f * err + 0x1p-21f * fmaxf(fabsf(in), fabsf(out));
       const bool unsure = done && !(in - out > room);
       if (__any_sync(kAll, unsure)) {
         // the last group kept against the first left out, in fp64
@@ -697,20 +754,44 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
             first = g, many += 16;
           }
         }
-        const bool here = unsure && many == 17 && (SIGMOID || !BIASED);   // (else slow_row's)
-        double rank[2] = {0.0, 0.0};
+        const bool here = unsure && many == 17;   // (else slow_row's)
+        // of their experts only those that fp32 leaves among the best
+        double rank[2] = {0.0, 0.0}, most = 0.0;   // (the largest uncertain part)
+        const double inv64 = exact_inv(largest, top2, inv);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int g = here ? (i == 0 ? last : first) : 0;
+          auto choice = [&](int j) {
+            const float s = score(in_shared(z + g * sh.wide + j));
+            return BIASED ? s + s_bias[g * (sh.wide + 4) + j] : s;
+          };
+          float one = -INFINITY, two = -INFINITY;
+#pragma unroll 1
+          for (int j = sub; here && j < sh.size; j += 4) {
+            const float c = choice(j);
+            two = fmaxf(two, fminf(one, c));
+            one = fmaxf(one, c);
+          }
+#pragma unroll 1
+          for (int o = 1; o < 4; o <<= 1) {
+            const float f = __shfl_xor_sync(kAll, one, o), s = __shfl_xor_sync(kAll, two, o);
+            two = fmaxf(fminf(one, f), fmaxf(two, s));
+            one = fmaxf(one, f);
+          }
+          const float least = a.top2 ? two : one, cut = least - 2.0f * err - 0x1p-21f * fabsf(least);
           double best = -INFINITY, next = -INFINITY;
 #pragma unroll 1
           for (int j = sub; here && j < sh.size; j += 4) {
-            const float x = in_shared(z + g * sh.size + j);
-            const double v = exact_score(SIGMOID ? static_cast<double>(x)
-                                                 : static_cast<double>(x) - static_cast<double>(largest), SIGMOID) +
-                             (BIASED ? static_cast<double>(s_bias[g * (sh.size + 4) + j]) : 0.0);
-            next = fmax(next, fmin(best, v));
-            best = fmax(best, v);
+            if (choice(j) < cut) continue;
+            const float x = in_shared(z + g * sh.wide + j);
+            // (without a bias every score has the same factor, which is left out)
+            const Choice c = BIASED ? exact_choice<SIGMOID, true>(x, s_bias[g * (sh.wide + 4) + j], largest, inv64)
+                                    : Choice{exact_score(SIGMOID ? static_cast<double>(x)
+                                                                 : static_cast<double>(x) - static_cast<double>(largest),
+                                                         SIGMOID), 0.0};
+            most = fmax(most, c.part);
+            next = fmax(next, fmin(best, c.value));
+            best = fmax(best, c.value);
           }
 #pragma unroll 1
           for (int o = 1; o < 4; o <<= 1) {
@@ -719,6 +800,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
             best = fmax(best, f);
           }
           rank[i] = a.top2 ? best + next : best;
+        }
+        if (!SIGMOID && BIASED) {
+          most = fmax(most, __shfl_xor_sync(kAll, most, 1));
+          most = fmax(most, __shfl_xor_sync(kAll, most, 2));
+          // (two values in each rank; the difference of the parts that count is at most 2 most)
+          if (here && fabs(rank[1] - rank[0]) <= 2.0 * static_cast<double>(rel) * most) done = false;
         }
         if (here && (rank[1] > rank[0] || (rank[1] == rank[0] && first < last))) kept ^= 1u << last | 1u << first;
         if (unsure && !here) done = false;
@@ -743,8 +830,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   for (int n = 0; n < a.keep; ++n) {
     const int g = kept ? __ffs(kept) - 1 : 0;   // (a row that holds a NaN may have kept fewer; it is not done here)
     kept &= kept - 1;
-    for (int j = 8 * sub; j < sh.size; j += 32) {
-      const int e = g * sh.size + j;
+    for (int j = 8 * sub; j < sh.wide; j += 32) {
+      const int e = g * sh.wide + j;
       float v[8], b[8];
       eight(z + e, v);
       if (BIASED) eight(s_bias + e + 4 * g, b);
@@ -765,9 +852,15 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
     }
   }
   // Beyond 40 an fp32 weight may underflow where its fp64 form does not.  (The
-  // sum of squares leaves the integer units, which bound this kernel, alone.)
-  if (__any_sync(kAll, !(squares < 1600.0f)))
-    for (int e = sub; e < a.experts; e += 4) done = done && fabsf(in_shared(z + e)) < 40.0f;   // (not of a NaN)
+  // sum of squares leaves the integer units, which bound this kernel, alone;
+  // the padding's are exact in it.)
+  const bool ends = ((sh.wide / 8 - 1) & 3) == sub;   // of a group's eights this thread has the last
+  const int padded = extra * (!grouped ? (ends ? 1 : 0) : a.groups % 4 == 0 ? a.groups / 4 : ends ? a.groups : 0);
+  if (__any_sync(kAll, !(squares < 1600.0f + kPad * kPad * static_cast<float>(padded))))
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g)
+      for (int j = sub; j < sh.size; j += 4)
+        done = done && fabsf(in_shared(z + g * sh.wide + j)) < 40.0f;   // (not of a NaN)
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
     int32_t k[8];
@@ -778,10 +871,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
   }
   // thread `sub` of the four has the choices sub and sub + 4
   int id[2];
-  auto expert = [&](int32_t key) { return min(sh.mask - (key & sh.mask), a.experts - 1); };
+  auto expert = [&](int32_t key) { return min(sh.mask - (key & sh.mask), sh.wide * a.groups - 1); };   // (its place)
   // two scores' errors and two roundings, in counts of the fixed point
-  constexpr int kRoom = BIASED ? static_cast<int>(2.0f * kErr * 0x1p20f) + 3 : 0;
-  auto near = [&](int32_t hi, int32_t lo) { return lo != kNone && (hi >> sh.bits) - (lo >> sh.bits) <= kRoom; };
+  const int room = BIASED ? static_cast<int>(2.0f * err * 0x1p20f) + 3 : 0;
+  auto near = [&](int32_t hi, int32_t lo) { return lo != kNone && (hi >> sh.bits) - (lo >> sh.bits) <= room; };
   bool close[2] = {false, false};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -820,7 +913,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
           left &= left - 1;
 #pragma unroll 1
           for (int j = sub; j < sh.size; j += 4) {
-            const int e = g * sh.size + j;
+            const int e = g * sh.wide + j;
             const int32_t k = key_at(in_shared(z + e), BIASED ? s_bias[e + 4 * g] : 0.0f, e);
             if (k < next) third = max(third, k);
           }
@@ -828,7 +921,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
         third = max(third, __shfl_xor_sync(kAll, third, 1));
         third = max(third, __shfl_xor_sync(kAll, third, 2));
       }
-      if ((pairs & (pairs << 1)) || (c[0] & c[1]) || (last && near(edge, third)) || (pairs && !SIGMOID && BIASED))
+      if ((pairs & (pairs << 1)) || (c[0] & c[1]) || (last && near(edge, third)))
         done = false;
       const int h = c[1] && (c[1] >> sub & 1u) ? 1 : 0;
       bool swap = false;
@@ -838,11 +931,14 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
         for (int i = 1; i < 8; ++i)
           if (i == sub + 4 * h + 1 && i < a.topk) after = top[i];
         const int e[2] = {h ? id[1] : id[0], expert(after)};
-        double v[2];
+        const double inv64 = exact_inv(largest, top2, inv);
+        Choice v[2];
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
-          v[i] = exact_choice<BIASED>(in_shared(z + e[i]) + 0.0f, BIASED ? s_bias[e[i] + 4 * (e[i] / sh.size)] : 0.0f);
-        swap = v[1] > v[0] || (v[1] == v[0] && e[1] < e[0]);
+          v[i] = exact_choice<SIGMOID, BIASED>(in_shared(z + e[i]) + 0.0f,
+                                               BIASED ? s_bias[e[i] + 4 * div_wide(e[i])] : 0.0f, largest, inv64);
+        swap = v[1].value > v[0].value || (v[1].value == v[0].value && e[1] < e[0]);
+        if (!SIGMOID && BIASED && unclear(v[0], v[1], rel)) done = false;
       }
       const uint32_t low = __ballot_sync(kAll, swap && h == 0) >> (lane & ~3) & 15u;
       const uint32_t high = __ballot_sync(kAll, swap && h == 1) >> (lane & ~3) & 15u;
@@ -884,7 +980,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 14) router_rows_kernel(const 
     for (int h = 0; h < 2; ++h)
       if (sub + 4 * h < a.topk) {
         const int64_t at = (t0 + own) * a.topk + sub + 4 * h;
-        a.ids[at] = id[h];
+        a.ids[at] = id[h] - div_wide(id[h]) * extra;
         a.weights[at] = w[h] * a.scale;
       }
   }
@@ -949,8 +1045,7 @@ cudaError_t launch_as(const RouterArgs& a, cudaStream_t st) {
 template <typename T>
 bool rows_fit(const RouterArgs& a) {
   return a.m >= kRowsLeast && a.topk <= kRowsTopk && a.topk < a.keep * (a.experts / a.groups) &&
-         (a.experts / a.groups) % 8 == 0 && a.experts * sizeof(T) <= kRowsBytes && a.experts * sizeof(T) % 16 == 0 &&
-         reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+         (a.experts / a.groups + 7) / 8 * 8 * a.groups <= kRowsPlaces;
 }
 template <typename T, bool SIGMOID, bool BIASED>
 cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
@@ -1014,9 +1109,10 @@ TQ_API int tq4_1s_router_scored(const void* logits, int dtype, int64_t m, const 
   int rc = check_device(nullptr);
   if (rc) return rc;
   if (take_injected_failure()) return TQ_ERR_CUDA;
+  const bool grouped = r->topk_groups < r->num_groups;   // (all of them kept: no groups)
   RouterArgs a{logits, bias,    ids,          weights,        m,
                r->num_experts,  r->topk,      r->score == TQ_SCORE_SIGMOID ? 1 : 0,
-               r->num_groups,   r->topk_groups, r->group_score == TQ_GROUP_TOP2 ? 1 : 0,
+               grouped ? r->num_groups : 1, grouped ? r->topk_groups : 1, r->group_score == TQ_GROUP_TOP2 ? 1 : 0,
                r->renormalize,  r->scale};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == TQ_DTYPE_F32 ? launch_pl<float>(a, st) : launch_pl<__nv_bfloat16>(a, st);

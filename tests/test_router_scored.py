@@ -371,3 +371,53 @@ def test_largest_biases_of_many_rows(E, score, edge):
     b[9] = -b[5]
     check(z, 8, b, score)
     check(z, 8, b, score, 4, 2, "top2")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m,E,topk,groups,keep,group_score,with_bias,renorm", [
+    (301, 250, 7, 1, 1, "max", False, True),         # rows that are no whole number of 16 bytes
+    (300, 245, 8, 1, 1, "max", True, True),
+    (1025, 200, 8, 8, 5, "top2", True, False),       # groups of 25
+    (515, 200, 3, 8, 5, "top2", False, True),
+    (270, 148, 6, 2, 1, "top2", True, True),         # groups of 74
+    (270, 60, 5, 4, 3, "max", True, True),           # groups of 15
+    (270, 36, 8, 12, 5, "top2", True, True),         # groups of 3
+    (270, 58, 2, 29, 1, "max", False, True),         # groups of 2, one kept, fewer than three
+    (400, 317, 4, 1, 1, "max", True, False),
+    (400, 511, 8, 7, 6, "max", True, True),          # as wide as they come: 7 x 80 places do not fit
+    (400, 497, 8, 7, 6, "top2", True, True),         # 7 x 72 do
+    (2048, 15, 8, 1, 1, "max", True, True),
+    (2048, 9, 8, 1, 1, "max", False, True),          # all but one
+    (256, 7, 6, 1, 1, "max", True, True),
+    (260, 2, 1, 1, 1, "max", True, True),
+])
+def test_many_rows_of_odd_sizes(m, E, topk, groups, keep, group_score, with_bias, renorm, score, dtype):
+    z = logits(m + 1, E, m + E, dtype)[1:] if E % 2 else logits(m, E, m + E, dtype)   # (off 16 bytes)
+    b = bias_of(E, E) if with_bias else None
+    check(z, topk, b, score, groups, keep, group_score, renorm, 2.5)
+    z[3] = 0.0
+    z[4] = -39.0
+    z[5] = 41.0
+    z[6, : E // 2] = -np.inf
+    z[m - 9] *= 30.0
+    check(z, topk, b, score, groups, keep, group_score, renorm)
+    assert tq.tq4_1s_get_status() == 0
+    if with_bias:
+        b[0], b[E - 1] = -2.5, 2.5
+        check(z, topk, b, score, groups, keep, group_score, renorm)
+    z[m - 1, E - 1] = np.nan
+    check(z, topk, b, score, groups, keep, group_score, renorm)
+    assert tq.tq4_1s_get_status() == tq.TQ_DEV_NONFINITE
+
+
+@pytest.mark.gpu
+def test_equal_bf16_logits_at_the_last_place():
+    # three and more equal logits around the last place: the lower ids, in either variant
+    for m in (30, 300):
+        z = logits(m, 250, m, torch.bfloat16)
+        z[:, 10::20] = 2.5
+        for topk in (1, 4, 8, 12):
+            check(z, topk, None, "softmax")
+            check(z, topk, None, "sigmoid", 5, 2, "max")
