@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* z, const
       e[j] = -1;
       if (j0 + j < topk) {
         v[j] = __ldcs(zt + static_cast<int64_t>(j0 + j) * hg);
-        e[j] = __ldcg(idt + j0 + j);
+        e[j] = idt[j0 + j];
       }
     }
 #pragma unroll
@@ -733,51 +733,51 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
     s.y = base + L.z;
     if (launch_int8_stream(TQ_DTYPE_BF16, td, s, tiles_dn, sms, st) != cudaSuccess) return TQ_ERR_CUDA;
   } else {
-  RowsArgs r{};
-  r.x = x;
-  r.ldx = r.k = H;
-  r.rows = m;
-  r.q = xq;
-  r.scale = f32(L.xscale);
-  r.ids = topk_ids;
-  r.topk = topk;
-  r.num_experts = static_cast<int32_t>(E);
-  r.cursor = i32(L.cursor);
-  r.pairs = i32(L.pairs);
-  r.topk_w = topk_w;
-  r.row_w = f32(L.row_w);
-  if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
-  Int8GemmArgs a{};
-  a.n = static_cast<int32_t>(I);
-  a.row_tiles = static_cast<int32_t>(rt_up);
-  a.ksteps = static_cast<int32_t>((H + 127) / 128);
-  a.mode = INT8_UP;
-  a.segs = segs;
-  a.nseg = i32(L.nseg);
-  a.xscale = f32(L.xscale);
-  a.wscale = up->wscale;
-  a.y = base + L.h;
-  if (launch_int8_gemm(tu, tx, a, L.nt, static_cast<int>(tiles_up < sms ? tiles_up : sms), st) != cudaSuccess)
-    return TQ_ERR_CUDA;
-  RowsArgs g{};
-  g.x = base + L.h;
-  g.ldx = g.k = I;
-  g.rows = L.slots;
-  g.q = hq;
-  g.scale = f32(L.hscale);
-  g.rows_dev = i32(L.nrows);
-  if (launch_rows(TQ_DTYPE_BF16, g, st) != cudaSuccess) return TQ_ERR_CUDA;
-  a.n = static_cast<int32_t>(H);
-  a.row_tiles = static_cast<int32_t>(rt_dn);
-  a.ksteps = static_cast<int32_t>((I + 127) / 128);
-  a.mode = INT8_DOWN;
-  a.xscale = f32(L.hscale);
-  a.wscale = down->wscale;
-  a.pairs = i32(L.pairs);
-  a.row_w = f32(L.row_w);
-  a.y = base + L.z;
-  if (launch_int8_gemm(td, th, a, L.nt, static_cast<int>(tiles_dn < sms ? tiles_dn : sms), st) != cudaSuccess)
-    return TQ_ERR_CUDA;
+    RowsArgs r{};
+    r.x = x;
+    r.ldx = r.k = H;
+    r.rows = m;
+    r.q = xq;
+    r.scale = f32(L.xscale);
+    r.ids = topk_ids;
+    r.topk = topk;
+    r.num_experts = static_cast<int32_t>(E);
+    r.cursor = i32(L.cursor);
+    r.pairs = i32(L.pairs);
+    r.topk_w = topk_w;
+    r.row_w = f32(L.row_w);
+    if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
+    Int8GemmArgs a{};
+    a.n = static_cast<int32_t>(I);
+    a.row_tiles = static_cast<int32_t>(rt_up);
+    a.ksteps = static_cast<int32_t>((H + 127) / 128);
+    a.mode = INT8_UP;
+    a.segs = segs;
+    a.nseg = i32(L.nseg);
+    a.xscale = f32(L.xscale);
+    a.wscale = up->wscale;
+    a.y = base + L.h;
+    if (launch_int8_gemm(tu, tx, a, L.nt, static_cast<int>(tiles_up < sms ? tiles_up : sms), st) != cudaSuccess)
+      return TQ_ERR_CUDA;
+    RowsArgs g{};
+    g.x = base + L.h;
+    g.ldx = g.k = I;
+    g.rows = L.slots;
+    g.q = hq;
+    g.scale = f32(L.hscale);
+    g.rows_dev = i32(L.nrows);
+    if (launch_rows(TQ_DTYPE_BF16, g, st) != cudaSuccess) return TQ_ERR_CUDA;
+    a.n = static_cast<int32_t>(H);
+    a.row_tiles = static_cast<int32_t>(rt_dn);
+    a.ksteps = static_cast<int32_t>((I + 127) / 128);
+    a.mode = INT8_DOWN;
+    a.xscale = f32(L.hscale);
+    a.wscale = down->wscale;
+    a.pairs = i32(L.pairs);
+    a.row_w = f32(L.row_w);
+    a.y = base + L.z;
+    if (launch_int8_gemm(td, th, a, L.nt, static_cast<int>(tiles_dn < sms ? tiles_dn : sms), st) != cudaSuccess)
+      return TQ_ERR_CUDA;
   }
   const int32_t hg = static_cast<int32_t>(H / 4), experts = static_cast<int32_t>(E);
   const unsigned blocks = static_cast<unsigned>((m * hg + 255) / 256);
