@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_con
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + (live ? row : 0) * a.ldx);
   uint4 raw[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) raw[i] = live && lane + i * TPR < nvec ? __ldcs(x + lane + i * TPR) : make_uint4(0, 0, 0, 0);
+  for (int i = 0; i < NV; ++i)
+    raw[i] = live && lane + i * TPR < nvec ? __ldcs(x + lane + i * TPR) : make_uint4(0, 0, 0, 0);
   if (SCATTER && live) take_rows(a, row, lane, TPR, s_at[sub]);
   uint32_t top = 0;
 #pragma unroll
@@ -621,7 +622,8 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   }
   uint8_t* base = static_cast<uint8_t*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + L.xq);
-  if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) || !encode_i8_map(&tx, xq, 0, m, w->k, p.nt == kInt8Pair ? 128 : p.nt))
+  if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128) ||
+      !encode_i8_map(&tx, xq, 0, m, w->k, p.nt == kInt8Pair ? 128 : p.nt))
     return TQ_ERR_CUDA;
   RowsArgs r{};
   r.x = x;

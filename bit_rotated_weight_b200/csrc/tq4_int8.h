@@ -27,7 +27,6 @@ struct Int8GemmArgs {
 // is 0 (2-D): box 128 bytes x box_rows, 128-byte swizzle, zeros outside.
 bool encode_i8_map(CUtensorMap* m, const int8_t* base, int64_t experts, int64_t rows, int64_t k, int box_rows);
 
-
 // nt: 16, 32, 64, 128 or 256 tokens a tile (the box rows of tx), or kInt8Pair:
 // dense tiles of 256 weight rows (row_tiles counts those) x 256 tokens shared
 // by two CTAs (an even grid), whose tx has 128 box rows.

@@ -16,7 +16,7 @@
 //              tokens x 6 of 128 experts took 262 us).
 // A tile that holds fewer than NT tokens multiplies only those, rounded up to 16.
 // Bound, in the grouped launches of 4096 tokens x 6 of 128 experts, by DRAM (up
-// 137 us for 795 MB, down 173 us for 947 MB: 5.8 and 5.5 TB/s); in dense ones
+// 135 us for 795 MB, down 165 us for 947 MB: 5.9 and 5.7 TB/s); in dense ones
 // of one wave by the latency of a k step, 0.23 us (512 x 4096 x 4096 13.5 us).
 // A tile's k is never cut between CTAs: with the parts left in memory and
 // summed by the CTA that ends last, 4096 x 4096 took 20 to 28 us at 32 to 128
@@ -345,8 +345,8 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 // cta_group::2, issued by the first CTA, read both halves; each CTA finishes
 // its own 128 rows.  The first CTA's `full` barriers count the bytes of both,
 // its commits free the stages of both, and its `dempty` counts the epilogue
-// warps of both.  Bound by the tensor cores: 8192 x 14336 x 4096 in 294 us, 3.3
-// POP/s, as a burst; 345 us under the power limit.  (Alone, a CTA's 48 KB a k
+// warps of both.  Bound by the tensor cores: 8192 x 14336 x 4096 in 286 us, 3.4
+// POP/s, as a burst; 335 to 350 us under the power limit.  (Alone, a CTA's 48 KB a k
 // step took 324 and 385 us.)
 constexpr int kPairTok = 256;
 constexpr int kPairStageBytes = kABytes + kPairTok / 2 * kStep;
@@ -535,7 +535,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 2) tmem_dealloc2(tmem, 512);
 }
 
-cudaError_t launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const Int8GemmArgs& a, int grid,
+                        cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
     return cudaFuncSetAttribute(int8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -36,8 +36,8 @@
 // (17 and 11 MB: 2.6 and 1.7 us of DRAM), a chain of latencies: the launch 2,
 // the tokens' loads 1.2, their maxima across the cluster 1, codes 0.5 to 1, the
 // MMAs 0.8, the exchange of sums 0.7.  The two projections of 16 tokens x 6 of
-// 128 experts (686 MB) 117 us, 5.9 TB/s, DRAM; those of one token (60 MB)
-// 16 us, 90 and 126 tiles for 148 SMs at 41 GB/s each.
+// 128 experts (686 MB) 112 us, 6.1 TB/s, DRAM; those of one token (60 MB)
+// 15 us, 90 and 126 tiles for 148 SMs at 41 GB/s each.
 #include "tq4_int8_mma.cuh"
 #include "tq4_int8_rows.cuh"
 
@@ -53,7 +53,7 @@ constexpr int kAcc = 64;                   // tensor-memory columns between the 
 constexpr int kMaxStages = 12;
 constexpr int kSpace = 208 * 1024;         // the tokens' codes and the weight stages
 constexpr int kHold = 4;                   // turns whose values a quantizer thread keeps between its two passes
-constexpr int kPartRow = 20;               // ints of a row's partial sums (16 and padding: 16-byte reads without conflicts)
+constexpr int kPartRow = 20;               // ints of a row's partial sums (16, and padding against bank conflicts)
 constexpr int kMaxParts = 8;
 
 struct Shared {
@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int me = warp - 1;
     int ti = 0, turn3 = 0;   // whose turn the tile's first k step is
     bool ok = true, fresh = true;   // the first tile of a segment
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abortp)) != 0; };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abortp)) != 0;
+    };
 #pragma unroll 1
     for (; ok && w.left > 0; w.next(), ++ti) {
       const int turn = w.seg - seg0, db = ti & 1;
