@@ -494,7 +494,7 @@ __device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plai
 // are near are told apart in fp64 in place, and so are two groups; what is left
 // (three that are near) is done again by the whole warp, which costs little
 // work but 10 us of fetching code that is otherwise not run.  (27447 x 148,
-// softmax with a bias: 11.7 us; 24.6 with its near pairs left to the warp, 43
+// softmax with a bias: 11.7 us; 24.6 with its near pairs left to the warp, 38
 // by a warp a row.)
 // 14 blocks of two warps an SM: 29.4 us for 65536 x 256, 30.3 for 10, 30.4 for 28
 // of one warp; warps that go on to their next rows, copied meanwhile, 32.5.

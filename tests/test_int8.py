@@ -742,3 +742,49 @@ def test_linear_few_tokens_back_to_back(m, n, k):
     want = torch.from_numpy(ref_fp32(acc, xs, s[0])).to(BF16)
     assert all(torch.equal(bits(y[:, rows.to(DEV)]), bits(want)) for y in ys)
     assert tq.tq4_1s_get_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m", [4, 16, 40, 300, 2400])
+def test_calls_read_what_the_call_before_wrote(m):
+    # each kernel may be set up while the one before it still runs: chains of calls without a pause, against calls that
+    # wait for the GPU, with fresh inputs in the same buffers
+    E = 128
+    w1 = tq.tq4_1s_int8_quantize(torch.randn(512, 256, generator=gen(m)).to(DEV))
+    w2 = tq.tq4_1s_int8_quantize(torch.randn(E, 512, generator=gen(m + 1)).to(DEV))
+    up = tq.tq4_1s_int8_quantize(torch.randn(E, 64, 256, generator=gen(m + 2)).to(DEV))
+    dn = tq.tq4_1s_int8_quantize(torch.randn(E, 256, 64, generator=gen(m + 3)).to(DEV))
+    x = torch.empty(m, 256, dtype=BF16, device=DEV)
+    bias = torch.randn(E, generator=gen(m + 4)).to(DEV)
+
+    def chain(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        h = tq.tq4_1s_linear_int8(x, w1)
+        pause()
+        z = tq.tq4_1s_linear_int8(h.float(), w2)
+        pause()
+        z2 = tq.tq4_1s_linear_int8(tq.tq4_1s_linear_int8(x, w1), w2)
+        pause()
+        ids, tw = tq.tq4_1s_router_scored(z2, 4, bias=bias, score="sigmoid", num_groups=8, topk_groups=3,
+                                          group_score="top2")
+        pause()
+        y = tq.tq4_1s_moe_int8(x, ids, tw, up, dn)
+        pause()
+        q = tq.tq4_1s_int8_quantize(y)
+        pause()
+        back = tq.tq4_1s_int8_dequantize(q)
+        pause()
+        last = tq.tq4_1s_linear_int8(y, tq.tq4_1s_int8_quantize(back.to(BF16)[0]))
+        pause()
+        return z, z2, ids, tw, y, q.q, q.wscale, back, last
+
+    g = gen(m + 5)
+    for _ in range(6):
+        fresh = torch.randn(m, 256, generator=g).to(BF16).to(DEV)
+        torch.cuda.synchronize()
+        x.copy_(fresh)
+        got = chain(False)
+        torch.cuda.synchronize()
+        want = chain(True)
+        for a, b in zip(got, want):
+            assert torch.equal(bits(a) if a.is_floating_point() else a, bits(b) if b.is_floating_point() else b)
