@@ -48,6 +48,103 @@ struct RowsArgs {
   float* row_w;
 };
 
+// Counts each expert's slots and writes the segments (at most `chunk` rows of
+// one expert), their number, the number of rows, and each expert's first row
+// (the scatter's cursors).  By one block; `count`: an int per expert, holds the
+// first rows in the end.
+struct SegmentArgs {
+  const int32_t* ids;
+  int64_t slots;
+  int32_t num_experts, chunk;
+  int32_t* cursor;
+  int4* segs;
+  int32_t* nseg;
+  int32_t* nrows;
+};
+template <int THREADS>
+__device__ __forceinline__ void segments_of(const SegmentArgs& a, int32_t* count) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ int32_t s_rows[kWarps], s_segs[kWarps];
+  __shared__ int32_t s_bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int e = tid; e < a.num_experts; e += THREADS) count[e] = 0;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  for (int64_t p0 = tid; p0 < a.slots; p0 += 8 * THREADS) {   // (eight loads in flight a thread)
+    int32_t e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = p0 + j * THREADS < a.slots ? __ldcg(a.ids + p0 + j * THREADS) : INT32_MIN;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (e[j] >= 0 && e[j] < a.num_experts) atomicAdd(&count[e[j]], 1);
+      else if (p0 + j * THREADS < a.slots) s_bad = 1;
+    }
+  }
+  __syncthreads();
+  int32_t rows0 = 0, segs0 = 0;   // of the experts before this pass
+  for (int e0 = 0; e0 < a.num_experts; e0 += THREADS) {
+    const int e = e0 + tid;
+    const int32_t c = e < a.num_experts ? count[e] : 0;
+    const int32_t ns = (c + a.chunk - 1) / a.chunk;
+    int32_t rows = c, nsegs = ns;   // inclusive scans: warp, then block
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t r = __shfl_up_sync(0xFFFFFFFFu, rows, o), s = __shfl_up_sync(0xFFFFFFFFu, nsegs, o);
+      if (lane >= o) {
+        rows += r;
+        nsegs += s;
+      }
+    }
+    if (lane == 31) {
+      s_rows[warp] = rows;
+      s_segs[warp] = nsegs;
+    }
+    __syncthreads();
+    int32_t total_r = 0, total_s = 0, before_r = rows0, before_s = segs0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        before_r += s_rows[w];
+        before_s += s_segs[w];
+      }
+      total_r += s_rows[w];
+      total_s += s_segs[w];
+    }
+    const int32_t row = before_r + rows - c, seg = before_s + nsegs - ns;
+    if (e < a.num_experts) {
+      a.cursor[e] = row;
+      count[e] = row;
+      for (int32_t i = 0; i < ns; ++i)
+        a.segs[seg + i] = make_int4(e, row + i * a.chunk, min(a.chunk, c - i * a.chunk), 0);
+    }
+    rows0 += total_r;
+    segs0 += total_s;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    *a.nseg = segs0;
+    *a.nrows = rows0;
+    if (s_bad) raise_status(TQ_DEV_BAD_ROUTING);
+  }
+}
+
+// With `pairs` the rows are given out here: the slot and weight of each sorted
+// row.
+__global__ void __launch_bounds__(1024) int8_segments_kernel(const __grid_constant__ SegmentArgs a, const float* topk_w,
+                                                             int32_t* pairs, float* row_w) {
+  extern __shared__ int32_t count[];
+  pdl_launch_dependents();
+  pdl_wait();
+  segments_of<1024>(a, count);
+  if (pairs)
+    for (int64_t p = threadIdx.x; p < a.slots; p += 1024) {
+      const int32_t e = a.ids[p];
+      if (e < 0 || e >= a.num_experts) continue;
+      const int32_t at = atomicAdd(&count[e], 1);
+      pairs[at] = static_cast<int32_t>(p);
+      row_w[at] = topk_w[p];
+    }
+}
+
 constexpr int kRowThreads = 256;
 
 // The destination rows of a scattered row (one expert slot each).
@@ -75,19 +172,60 @@ __device__ __forceinline__ void put_scale(const RowsArgs& a, int64_t row, int la
   }
 }
 
+// How a row finds its places: it has one (its own), one per slot, taken from the
+// experts' cursors, or counts them itself among at most kCountSlots ids (a
+// kernel less, as the grid's last block writes the segments meanwhile: 134
+// tokens x 4 of 8 small experts 20.2 -> 16.5 us, at 1996 slots 26.5 -> 24.7).
+enum Places { kOwnRow = 0, kCursors = 1, kCounts = 2 };
+constexpr int kCountSlots = 2048;
+
+// The places of the block's rows: the slots with a smaller id, and those with
+// the same one earlier.  A warp a slot.
+__device__ __forceinline__ void count_rows(const RowsArgs& a, int64_t row0, int rows, int32_t* ids, int32_t (*s_at)[64]) {
+  const int slots = static_cast<int>(a.rows) * a.topk, lane = threadIdx.x & 31;
+  for (int p = threadIdx.x; p < slots; p += kRowThreads) ids[p] = __ldcg(a.ids + p);
+  __syncthreads();
+  for (int q = threadIdx.x >> 5; q < rows * a.topk; q += kRowThreads / 32) {
+    const int sub = q / a.topk, j = q - sub * a.topk;
+    const int slot = static_cast<int>(row0 + sub) * a.topk + j;
+    if (row0 + sub >= a.rows) break;
+    const int32_t e = ids[slot];
+    const bool valid = e >= 0 && e < a.num_experts;
+    int at = 0;
+#pragma unroll 4
+    for (int p = lane; p < slots; p += 32) at += (ids[p] >= 0 && ids[p] < e) || (ids[p] == e && p < slot) ? 1 : 0;
+    at = __reduce_add_sync(0xFFFFFFFFu, at);
+    if (lane == 0) {
+      s_at[sub][j] = valid ? at : -1;
+      if (valid) {
+        a.pairs[at] = slot;
+        a.row_w[at] = a.topk_w[slot];
+      }
+    }
+  }
+  __syncthreads();
+}
+
 // TPR threads hold a row of at most TPR * NV 16-byte vectors in registers: one
 // pass over the data, all of a thread's loads in flight at once.  Bound by
 // DRAM: 14336 x 4096 bf16 in 33.6 us, 5.2 TB/s of reads and writes; fp32 in
 // 45.6 us, 6.4 TB/s.
-template <typename T, int TPR, int NV, bool SCATTER>
-__global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_constant__ RowsArgs a) {
+template <typename T, int TPR, int NV, int PLACES>
+__global__ void __launch_bounds__(kRowThreads)
+    int8_rows_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ SegmentArgs sa) {
   using V = Vec<T>;
+  constexpr bool SCATTER = PLACES != kOwnRow;
+  extern __shared__ int32_t s_ids[];
   constexpr int kRowsPerBlock = kRowThreads / TPR;
   __shared__ uint32_t s_top[kRowThreads / 32];
   __shared__ int32_t s_at[SCATTER ? kRowsPerBlock : 1][64];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   pdl_wait();
   if (threadIdx.x == 0) pdl_launch_dependents();
+  if (PLACES == kCounts && blockIdx.x == gridDim.x - 1) {
+    segments_of<kRowThreads>(sa, s_ids);
+    return;
+  }
   const int64_t rows = a.rows_dev ? __ldcg(a.rows_dev) : a.rows;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + sub;
   const bool live = row < rows;
@@ -98,7 +236,8 @@ __global__ void __launch_bounds__(kRowThreads) int8_rows_kernel(const __grid_con
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     raw[i] = live && lane + i * TPR < nvec ? __ldcs(x + lane + i * TPR) : make_uint4(0, 0, 0, 0);
-  if (SCATTER && live) take_rows(a, row, lane, TPR, s_at[sub]);
+  if (PLACES == kCursors && live) take_rows(a, row, lane, TPR, s_at[sub]);
+  if (PLACES == kCounts) count_rows(a, static_cast<int64_t>(blockIdx.x) * kRowsPerBlock, kRowsPerBlock, s_ids, s_at);
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) top = max(top, V::top(raw[i]));
@@ -258,111 +397,45 @@ __global__ void __launch_bounds__(256) int8_combine_kernel(const float* z, const
   *(reinterpret_cast<uint2*>(y) + i) = o;
 }
 
-// Counts each expert's slots and writes the segments (at most `chunk` rows of
-// one expert), their number, the number of rows, and each expert's first row
-// (the scatter's cursors).  With `pairs` the rows are given out here: the slot
-// and weight of each sorted row.  One block: the slots are few bytes.
-__global__ void __launch_bounds__(1024) int8_segments_kernel(const int32_t* ids, int64_t slots, int32_t num_experts,
-                                                             int32_t chunk, int32_t* cursor, int4* segs, int32_t* nseg,
-                                                             int32_t* nrows, const float* topk_w, int32_t* pairs,
-                                                             float* row_w) {
-  extern __shared__ int32_t count[];
-  __shared__ int32_t s_rows[32], s_segs[32];
-  __shared__ int32_t s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_launch_dependents();
-  pdl_wait();
-  for (int e = tid; e < num_experts; e += 1024) count[e] = 0;
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  for (int64_t p0 = tid; p0 < slots; p0 += 8 * 1024) {   // (eight loads in flight a thread)
-    int32_t e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = p0 + j * 1024 < slots ? __ldcg(ids + p0 + j * 1024) : INT32_MIN;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (e[j] >= 0 && e[j] < num_experts) atomicAdd(&count[e[j]], 1);
-      else if (p0 + j * 1024 < slots) s_bad = 1;
+template <typename T, int TPR, int NV>
+cudaError_t launch_rows_as(const RowsArgs& a, cudaLaunchConfig_t& cfg, const SegmentArgs* sa = nullptr) {
+  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kRowThreads / TPR - 1) / (kRowThreads / TPR)));
+  const SegmentArgs none{};
+  if constexpr (TPR >= 128)
+    if (sa) {
+      cfg.gridDim.x += 1;
+      cfg.dynamicSmemBytes = 4 * static_cast<size_t>(sa->slots > sa->num_experts ? sa->slots : sa->num_experts);
+      return cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, kCounts>, a, *sa);
     }
-  }
-  __syncthreads();
-  int32_t rows0 = 0, segs0 = 0;   // of the experts before this pass
-  for (int e0 = 0; e0 < num_experts; e0 += 1024) {
-    const int e = e0 + tid;
-    const int32_t c = e < num_experts ? count[e] : 0;
-    const int32_t ns = (c + chunk - 1) / chunk;
-    int32_t rows = c, nsegs = ns;   // inclusive scans: warp, then block
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t r = __shfl_up_sync(0xFFFFFFFFu, rows, o), s = __shfl_up_sync(0xFFFFFFFFu, nsegs, o);
-      if (lane >= o) {
-        rows += r;
-        nsegs += s;
-      }
-    }
-    if (lane == 31) {
-      s_rows[warp] = rows;
-      s_segs[warp] = nsegs;
-    }
-    __syncthreads();
-    int32_t total_r = 0, total_s = 0, before_r = rows0, before_s = segs0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) {
-        before_r += s_rows[w];
-        before_s += s_segs[w];
-      }
-      total_r += s_rows[w];
-      total_s += s_segs[w];
-    }
-    const int32_t row = before_r + rows - c, seg = before_s + nsegs - ns;
-    if (e < num_experts) {
-      cursor[e] = row;
-      count[e] = row;
-      for (int32_t i = 0; i < ns; ++i) segs[seg + i] = make_int4(e, row + i * chunk, min(chunk, c - i * chunk), 0);
-    }
-    rows0 += total_r;
-    segs0 += total_s;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    *nseg = segs0;
-    *nrows = rows0;
-    if (s_bad) raise_status(TQ_DEV_BAD_ROUTING);
-  }
-  if (pairs)
-    for (int64_t p = tid; p < slots; p += 1024) {
-      const int32_t e = ids[p];
-      if (e < 0 || e >= num_experts) continue;
-      const int32_t at = atomicAdd(&count[e], 1);
-      pairs[at] = static_cast<int32_t>(p);
-      row_w[at] = topk_w[p];
-    }
+  return a.ids ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, kCursors>, a, none)
+               : cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, kOwnRow>, a, none);
 }
 
-template <typename T, int TPR, int NV>
-cudaError_t launch_rows_as(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
-  cfg.gridDim = dim3(static_cast<unsigned>((a.rows + kRowThreads / TPR - 1) / (kRowThreads / TPR)));
-  return a.ids ? cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, true>, a)
-               : cudaLaunchKernelEx(&cfg, int8_rows_kernel<T, TPR, NV, false>, a);
+// Whether the rows can count their places themselves (those that do are long
+// or few enough for 128 threads each).
+template <typename T>
+bool rows_count(const RowsArgs& a) {
+  return a.rows * a.topk <= kCountSlots && a.k / Vec<T>::N <= 256 * 8 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
+         a.ldx % Vec<T>::N == 0;
 }
 
 template <typename T>
-cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg) {
+cudaError_t launch_rows_of(const RowsArgs& a, cudaLaunchConfig_t& cfg, const SegmentArgs* sa) {
   const int64_t nvec = a.k / Vec<T>::N;
   const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx % Vec<T>::N == 0;
   // Many rows: a warp each up to 4 KB (24576 x 1856 bf16 24.0 us, 28.8 with two
   // warps), four warps up to 16 KB (14336 x 4096 bf16 33.6 us, 78.7 with one;
   // fp32 45.6 us, 48.6 with eight).  Few: as many threads as there are pieces.
-  if (wide && a.rows >= 148 * 8) {
+  if (wide && !sa && a.rows >= 148 * 8) {
     if (nvec <= 32 * 4) return launch_rows_as<T, 32, 4>(a, cfg);
     if (nvec <= 32 * 8) return launch_rows_as<T, 32, 8>(a, cfg);
     if (nvec <= 128 * 4) return launch_rows_as<T, 128, 4>(a, cfg);
     if (nvec <= 128 * 8) return launch_rows_as<T, 128, 8>(a, cfg);
   }
-  if (wide && nvec <= 128) return launch_rows_as<T, 128, 1>(a, cfg);
-  if (wide && nvec <= 256 * 2) return launch_rows_as<T, 256, 2>(a, cfg);
-  if (wide && nvec <= 256 * 4) return launch_rows_as<T, 256, 4>(a, cfg);
-  if (wide && nvec <= 256 * 8) return launch_rows_as<T, 256, 8>(a, cfg);
+  if (wide && nvec <= 128) return launch_rows_as<T, 128, 1>(a, cfg, sa);
+  if (wide && nvec <= 256 * 2) return launch_rows_as<T, 256, 2>(a, cfg, sa);
+  if (wide && nvec <= 256 * 4) return launch_rows_as<T, 256, 4>(a, cfg, sa);
+  if (wide && nvec <= 256 * 8) return launch_rows_as<T, 256, 8>(a, cfg, sa);
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
   return cudaLaunchKernelEx(&cfg, int8_rows_any_kernel<T>, a);
 }
@@ -384,13 +457,13 @@ void launch_early(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, unsigned g
   cfg.numAttrs = 1;
 }
 
-cudaError_t launch_rows(int dtype, const RowsArgs& a, cudaStream_t st) {
+cudaError_t launch_rows(int dtype, const RowsArgs& a, cudaStream_t st, const SegmentArgs* sa = nullptr) {
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   launch_early(cfg, attr, 1, kRowThreads, 0, st);   // (the grid is set below)
-  const cudaError_t e = dtype == TQ_DTYPE_F32    ? launch_rows_of<float>(a, cfg)
-                        : dtype == TQ_DTYPE_BF16 ? launch_rows_of<__nv_bfloat16>(a, cfg)
-                                                 : launch_rows_of<__half>(a, cfg);
+  const cudaError_t e = dtype == TQ_DTYPE_F32    ? launch_rows_of<float>(a, cfg, sa)
+                        : dtype == TQ_DTYPE_BF16 ? launch_rows_of<__nv_bfloat16>(a, cfg, sa)
+                                                 : launch_rows_of<__half>(a, cfg, sa);
   if (e != cudaSuccess) return e;
   note_launches(1);
   return cudaGetLastError();
@@ -489,7 +562,7 @@ MoeLayout moe_layout(int64_t m, int32_t topk, int64_t experts, int64_t H, int64_
   // x 6: 237 us at 64 and 128, 243 at 32, 261 at 256); from 136 on it is the MMAs
   // (4096 tokens: 456 us at 256, 507 at 128; 2048: 351 and 321).
   // Of few rows it is the launches, and the form without quantizing kernels
-  // (16) is shorter, three launches against six: 16 x 8 slots of 128 experts of
+  // (16) is shorter, three launches against five: 16 x 8 slots of 128 experts of
   // 2688 x 1856 138 us and 143, of 1088 x 896 39 and 49; 32 slots of 4 experts of
   // 512 x 512 14 and 16.5.  But there every CTA quantizes its experts' rows
   // itself, which pays up to about 16384 values an expert: 111 slots of 30
@@ -688,12 +761,29 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
     return TQ_ERR_CUDA;
   // and where the slots fit a block's routing they need no kernel for that
   const bool routed = stream_rows && L.slots <= kStreamSlots;
-  if (!routed) {
+  const SegmentArgs sa{topk_ids,      L.slots, static_cast<int32_t>(E), L.nt, i32(L.cursor), segs,
+                       i32(L.nseg),   i32(L.nrows)};
+  RowsArgs r{};
+  r.x = x;
+  r.ldx = r.k = H;
+  r.rows = m;
+  r.q = xq;
+  r.scale = f32(L.xscale);
+  r.ids = topk_ids;
+  r.topk = topk;
+  r.num_experts = static_cast<int32_t>(E);
+  r.cursor = i32(L.cursor);
+  r.pairs = i32(L.pairs);
+  r.topk_w = topk_w;
+  r.row_w = f32(L.row_w);
+  // (where the rows count their places, their kernel writes the segments too)
+  const bool counted =
+      !stream_rows && (dtype == TQ_DTYPE_BF16 ? rows_count<__nv_bfloat16>(r) : rows_count<__half>(r));
+  if (!routed && !counted) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr;
     launch_early(cfg, attr, 1, 1024, static_cast<size_t>(E) * 4, st);
-    if (cudaLaunchKernelEx(&cfg, int8_segments_kernel, topk_ids, L.slots, static_cast<int32_t>(E),
-                           static_cast<int32_t>(L.nt), i32(L.cursor), segs, i32(L.nseg), i32(L.nrows), topk_w,
+    if (cudaLaunchKernelEx(&cfg, int8_segments_kernel, sa, topk_w,
                            stream_rows ? i32(L.pairs) : static_cast<int32_t*>(nullptr), f32(L.row_w)) != cudaSuccess)
       return TQ_ERR_CUDA;
     note_launches(1);
@@ -735,20 +825,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
     s.y = base + L.z;
     if (launch_int8_stream(TQ_DTYPE_BF16, td, s, tiles_dn, sms, st) != cudaSuccess) return TQ_ERR_CUDA;
   } else {
-    RowsArgs r{};
-    r.x = x;
-    r.ldx = r.k = H;
-    r.rows = m;
-    r.q = xq;
-    r.scale = f32(L.xscale);
-    r.ids = topk_ids;
-    r.topk = topk;
-    r.num_experts = static_cast<int32_t>(E);
-    r.cursor = i32(L.cursor);
-    r.pairs = i32(L.pairs);
-    r.topk_w = topk_w;
-    r.row_w = f32(L.row_w);
-    if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
+    if (launch_rows(dtype, r, st, counted ? &sa : nullptr) != cudaSuccess) return TQ_ERR_CUDA;
     Int8GemmArgs a{};
     a.n = static_cast<int32_t>(I);
     a.row_tiles = static_cast<int32_t>(rt_up);

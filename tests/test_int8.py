@@ -788,3 +788,23 @@ def test_calls_read_what_the_call_before_wrote(m):
         want = chain(True)
         for a, b in zip(got, want):
             assert torch.equal(bits(a) if a.is_floating_point() else a, bits(b) if b.is_floating_point() else b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,E,topk", [(100, 8, 3), (256, 8, 8), (257, 8, 8), (900, 1100, 2), (33, 40, 64)])
+def test_moe_bad_ids_of_more_tokens(m, E, topk):
+    # slots that are counted by the rows themselves (up to 2048), by a kernel of their own, of more experts than threads
+    up, down, ru, rd = moe_weights(E, 64, 96, 46)
+    ids, tw = routing(m, E, topk, 47) if topk <= E else (np.random.default_rng(5).integers(0, E, (m, topk)).astype(np.int32),
+                                                         np.random.default_rng(6).random((m, topk)).astype(np.float32))
+    ids[0] = -1
+    ids[1] = ids[2]                                        # two tokens alike
+    ids[5, 1] = E
+    ids[m - 1, topk - 1] = 2 ** 31 - 1
+    ids[7, 0] = -(2 ** 31)
+    x = torch.randn(m, 64, generator=gen(48)).to(BF16)
+    y = check_moe(x, ids, tw, up, down, ru, rd)
+    assert bool((y[0] == 0).all()) and tq.tq4_1s_get_status() == tq.TQ_DEV_BAD_ROUTING
+    tq.tq4_1s_moe_int8(x.to(DEV), torch.full((m, topk), -1, dtype=torch.int32, device=DEV), torch.from_numpy(tw).to(DEV),
+                       up, down, out=y)
+    assert bool((y == 0).all())
