@@ -482,8 +482,8 @@ __device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plai
 // ------------------------------------------------------------------ many rows
 // Four threads per token, eight tokens a warp: next to no shuffles and no idle
 // lanes.  The rows lie in shared memory; eight experts at a time are turned
-// into keys, sorted by a network and merged into the thread's eight largest,
-// and the four threads' eights at the end.
+// into keys, sorted by a network and merged into the thread's 8 or 16 largest,
+// and the four threads' lists at the end.
 //
 // A key's lowest bits hold the expert (all ones minus it).  Above them stand
 // the highest bits of a logit's own key, or, with a bias, the choice value in
@@ -499,7 +499,7 @@ __device__ __noinline__ void again_row(const RouterArgs& a, int64_t t, bool plai
 // 14 blocks of two warps an SM: 29.4 us for 65536 x 256, 30.3 for 10, 30.4 for 28
 // of one warp; warps that go on to their next rows, copied meanwhile, 32.5.
 constexpr int kRowsWarps = 2, kRowsBlocks = 14;
-constexpr int kRowsTopk = 8;
+constexpr int kRowsTopk = 16;
 constexpr int kRowsOf = 8;         // tokens of a warp
 constexpr int kRowsPlaces = 512;   // nine bits
 constexpr int kRowsLeast = 256;
@@ -518,18 +518,21 @@ __device__ __forceinline__ void sort8(int32_t (&k)[8]) {
   order2(k[2], k[4]), order2(k[3], k[5]);
   order2(k[1], k[2]), order2(k[3], k[4]), order2(k[5], k[6]);
 }
-// Keeps the eight largest of two sorted eights, sorted; `lost`: the largest of the rest.
-__device__ __forceinline__ void merge8(int32_t (&top)[8], const int32_t (&k)[8], int32_t& lost) {
+// Keeps the K largest of two sorted lists (K and N of them), sorted; `lost`: the
+// largest of the rest.
+template <int K, int N>
+__device__ __forceinline__ void merge(int32_t (&top)[K], const int32_t (&k)[N], int32_t& lost) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    lost = max(lost, max(min(top[i], k[7 - i]), min(top[i + 1], k[6 - i])));
-    top[i] = max(top[i], k[7 - i]);
-    top[i + 1] = max(top[i + 1], k[6 - i]);
+  for (int i = 0; i < N; i += 2) {
+    int32_t &a = top[K - N + i], &b = top[K - N + i + 1];
+    lost = max(lost, max(min(a, k[N - 1 - i]), min(b, k[N - 2 - i])));
+    a = max(a, k[N - 1 - i]);
+    b = max(b, k[N - 2 - i]);
   }
 #pragma unroll
-  for (int d = 4; d > 0; d >>= 1)
+  for (int d = K / 2; d > 0; d >>= 1)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < K; ++i)
       if (!(i & d)) order2(top[i], top[i + d]);
 }
 
@@ -597,7 +600,8 @@ RowsShape rows_shape(const RouterArgs& a) {
   return s;
 }
 
-template <typename T, bool SIGMOID, bool BIASED>
+// K: the largest keys that are kept (topk and more).
+template <typename T, int K, bool SIGMOID, bool BIASED>
 __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kernel(const __grid_constant__ RouterArgs a,
                                                                          const __grid_constant__ RowsShape sh) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -823,10 +827,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
     if (BIASED) return static_cast<int32_t>(__float_as_uint(c + offset) * unit + static_cast<uint32_t>(sh.mask - e));
     return (key_of(c) & ~sh.mask) | (sh.mask - e);
   };
-  int32_t top[8], lost = kNone;
+  int32_t top[K], lost = kNone;
   const uint32_t stay = kept;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top[i] = kNone;
+  for (int i = 0; i < K; ++i) top[i] = kNone;
   bool empty = true;
   for (int n = 0; n < a.keep; ++n) {
     const int g = kept ? __ffs(kept) - 1 : 0;   // (a row that holds a NaN may have kept fewer; it is not done here)
@@ -848,7 +852,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
         for (int i = 0; i < 8; ++i) top[i] = k[i];
         empty = false;
       } else {
-        merge8(top, k, lost);
+        merge<K, 8>(top, k, lost);
       }
     }
   }
@@ -864,48 +868,56 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
         done = done && fabsf(in_shared(z + g * sh.wide + j)) < 40.0f;   // (not of a NaN)
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) {
-    int32_t k[8];
+    int32_t k[K];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = __shfl_xor_sync(kAll, top[i], o);
+    for (int i = 0; i < K; ++i) k[i] = __shfl_xor_sync(kAll, top[i], o);
     lost = max(lost, __shfl_xor_sync(kAll, lost, o));
-    merge8(top, k, lost);
+    merge<K, K>(top, k, lost);
   }
-  // thread `sub` of the four has the choices sub and sub + 4
-  int id[2];
+  // thread `sub` of the four has the choices sub, sub + 4, ...
+  constexpr int kOwn = K / 4;
+  int id[kOwn];
   auto expert = [&](int32_t key) { return min(sh.mask - (key & sh.mask), sh.wide * a.groups - 1); };   // (its place)
   // two scores' errors and two roundings, in counts of the fixed point
   const int room = BIASED ? static_cast<int>(2.0f * err * 0x1p20f) + 3 : 0;
   auto near = [&](int32_t hi, int32_t lo) { return lo != kNone && (hi >> sh.bits) - (lo >> sh.bits) <= room; };
-  bool close[2] = {false, false};
+  bool close[kOwn];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kOwn; ++h) {
     int32_t key = top[4 * h], after = top[4 * h + 1];
 #pragma unroll
     for (int i = 1; i < 4; ++i)
       if (sub == i) {
         key = top[4 * h + i];
-        after = 4 * h + i < 7 ? top[4 * h + i + 1] : lost;
+        after = 4 * h + i < K - 1 ? top[4 * h + i + 1] : lost;
       }
     id[h] = expert(key);
     // (a bf16 logit's key holds all of it)
-    if (BIASED || sizeof(T) == 4) close[h] = sub + 4 * h < a.topk && near(key, after);
+    close[h] = (BIASED || sizeof(T) == 4) && sub + 4 * h < a.topk && near(key, after);
   }
   if (BIASED || sizeof(T) == 4) {
-    const uint32_t c[2] = {__ballot_sync(kAll, close[0] && done) >> (lane & ~3) & 15u,
-                           __ballot_sync(kAll, close[1] && done) >> (lane & ~3) & 15u};
-    const uint32_t pairs = c[0] | c[1] << 4;   // bit j: choices j and j + 1 of this row are near
+    uint32_t pairs = 0, one = 0, two = 0;   // bit j: choices j and j + 1 of this row are near; threads with one, two
+    int h = 0;                              // which of this thread's choices
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const uint32_t c = __ballot_sync(kAll, close[i] && done) >> (lane & ~3) & 15u;
+      pairs |= c << (4 * i);
+      two |= one & c;
+      one |= c;
+      if (i > 0 && (c >> sub & 1u)) h = i;
+    }
     if (__any_sync(kAll, pairs != 0)) {
       // Each such pair by its values in fp64.  Left to fast_row: three in a
       // row, a last place that two others are near, and two pairs of a thread.
       int32_t edge = kNone, third = lost, next = lost;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < K; ++i) {
         if (i == a.topk - 1) edge = top[i];
         if (i == a.topk) next = top[i];
         if (i == a.topk + 1) third = top[i];
       }
       const bool last = (pairs >> (a.topk - 1)) & 1u;
-      if (a.topk == 8 && __any_sync(kAll, last)) {   // the largest below `next` was not kept
+      if (a.topk == K && __any_sync(kAll, last)) {   // the largest below `next` was not kept
         third = kNone;
         uint32_t left = stay;
 #pragma unroll 1
@@ -922,16 +934,18 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
         third = max(third, __shfl_xor_sync(kAll, third, 1));
         third = max(third, __shfl_xor_sync(kAll, third, 2));
       }
-      if ((pairs & (pairs << 1)) || (c[0] & c[1]) || (last && near(edge, third)))
-        done = false;
-      const int h = c[1] && (c[1] >> sub & 1u) ? 1 : 0;
+      if ((pairs & (pairs << 1)) || two || (last && near(edge, third))) done = false;
       bool swap = false;
       if (done && ((pairs >> (sub + 4 * h)) & 1u)) {
         int32_t after = next;
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+        for (int i = 1; i < K; ++i)
           if (i == sub + 4 * h + 1 && i < a.topk) after = top[i];
-        const int e[2] = {h ? id[1] : id[0], expert(after)};
+        int chosen = id[0];
+#pragma unroll
+        for (int i = 1; i < kOwn; ++i)
+          if (i == h) chosen = id[i];
+        const int e[2] = {chosen, expert(after)};
         const double inv64 = exact_inv(largest, top2, inv);
         Choice v[2];
 #pragma unroll 1
@@ -941,15 +955,15 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
         swap = v[1].value > v[0].value || (v[1].value == v[0].value && e[1] < e[0]);
         if (!SIGMOID && BIASED && unclear(v[0], v[1], rel)) done = false;
       }
-      const uint32_t low = __ballot_sync(kAll, swap && h == 0) >> (lane & ~3) & 15u;
-      const uint32_t high = __ballot_sync(kAll, swap && h == 1) >> (lane & ~3) & 15u;
-      const uint32_t swaps = low | high << 4;   // bit j: choices j and j + 1 of this row change places
+      uint32_t swaps = 0;   // bit j: choices j and j + 1 of this row change places
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int i = 0; i < kOwn; ++i) swaps |= (__ballot_sync(kAll, swap && h == i) >> (lane & ~3) & 15u) << (4 * i);
+#pragma unroll
+      for (int g = 0; g < kOwn; ++g) {
         const int j = sub + 4 * g;
         int32_t key = kNone;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < K; ++i) {
           if (i == j + 1 && i < a.topk && (swaps >> j & 1u)) key = top[i];
           if (i + 1 == j && (swaps >> i & 1u)) key = top[i];
         }
@@ -958,9 +972,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
       }
     }
   }
-  float w[2];
+  float w[kOwn];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kOwn; ++h) {
     w[h] = 0.0f;
     if (sub + 4 * h < a.topk) {
       const float x = in_shared(z + id[h]);
@@ -968,17 +982,19 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
     }
   }
   if (a.renorm) {   // summed in the order of fast_row's shuffles: the same bits
-    float total = w[0] + w[1];
+    float total;
+    if constexpr (K == 16) total = (w[0] + w[2]) + (w[1] + w[3]);
+    else total = w[0] + w[1];
     total += __shfl_xor_sync(kAll, total, 2);
     const float f = rcp(total + __shfl_xor_sync(kAll, total, 1));
-    w[0] *= f;
-    w[1] *= f;
+#pragma unroll
+    for (int h = 0; h < kOwn; ++h) w[h] *= f;
   }
   const uint32_t undone = __ballot_sync(kAll, !done && own < rows);   // (no thread needs the rows any more)
   const bool redo = ((undone >> (lane & ~3)) & 15u) != 0;
   if (!redo && own < rows) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < kOwn; ++h)
       if (sub + 4 * h < a.topk) {
         const int64_t at = (t0 + own) * a.topk + sub + 4 * h;
         a.ids[at] = id[h] - div_wide(id[h]) * extra;
@@ -1049,11 +1065,11 @@ bool rows_fit(const RouterArgs& a) {
   return a.m >= kRowsLeast && a.topk <= kRowsTopk && a.topk < a.keep * (a.experts / a.groups) &&
          (a.experts / a.groups + 7) / 8 * 8 * a.groups <= kRowsPlaces;
 }
-template <typename T, bool SIGMOID, bool BIASED>
-cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
+template <typename T, int K, bool SIGMOID, bool BIASED>
+cudaError_t launch_rows_of(const RouterArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
   const cudaError_t e = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(router_rows_kernel<T, SIGMOID, BIASED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(router_rows_kernel<T, K, SIGMOID, BIASED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 160 * 1024);
   });
   if (e != cudaSuccess) return e;
@@ -1063,10 +1079,17 @@ cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
   cudaLaunchAttribute attr;
   launch_early(cfg, attr, static_cast<unsigned>((a.m + rows - 1) / rows), kRowsWarps * 32,
                s.bias_floats * 4 + kRowsWarps * s.warp_bytes, st);
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, router_rows_kernel<T, SIGMOID, BIASED>, a, s);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, router_rows_kernel<T, K, SIGMOID, BIASED>, a, s);
   if (r != cudaSuccess) return r;
   note_launches(1);
   return cudaGetLastError();
+}
+
+// 8 keys a thread, or 16, which cost more: 65536 x 256 28 us and 32 (a warp a row,
+// topk = 9: 80).
+template <typename T, bool SIGMOID, bool BIASED>
+cudaError_t launch_rows(const RouterArgs& a, cudaStream_t st) {
+  return a.topk <= 8 ? launch_rows_of<T, 8, SIGMOID, BIASED>(a, st) : launch_rows_of<T, 16, SIGMOID, BIASED>(a, st);
 }
 
 template <typename T>

@@ -421,3 +421,50 @@ def test_equal_bf16_logits_at_the_last_place():
         for topk in (1, 4, 8, 12):
             check(z, topk, None, "softmax")
             check(z, topk, None, "sigmoid", 5, 2, "max")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m,E,topk,groups,keep,group_score,with_bias,renorm", [
+    (300, 256, 9, 8, 4, "top2", True, True),
+    (1031, 256, 16, 8, 4, "top2", True, True),       # as many as a thread keeps
+    (300, 128, 12, 1, 1, "max", False, True),
+    (300, 17, 16, 1, 1, "max", True, True),          # all but one
+    (300, 24, 15, 4, 3, "max", True, False),
+    (300, 500, 13, 1, 1, "max", True, True),
+    (300, 96, 11, 12, 2, "top2", False, False),
+    (300, 64, 17, 1, 1, "max", True, True),          # one more than that form takes
+])
+def test_many_rows_of_many_choices(m, E, topk, groups, keep, group_score, with_bias, renorm, score, dtype):
+    z = logits(m, E, m + E + topk, dtype)
+    b = bias_of(E, E) if with_bias else None
+    check(z, topk, b, score, groups, keep, group_score, renorm, 2.5)
+    z[3], z[4], z[5] = 0.0, -39.0, 41.0
+    z[6, : E // 2] = -np.inf
+    check(z, topk, b, score, groups, keep, group_score, renorm)
+    # the same bits as in the form of few rows
+    few = tq.tq4_1s_router_scored(z[:200].contiguous(), topk, bias=None if b is None else b.to(DEV), score=score,
+                                  num_groups=groups, topk_groups=keep, group_score=group_score, renormalize=renorm)
+    many = tq.tq4_1s_router_scored(z, topk, bias=None if b is None else b.to(DEV), score=score,
+                                   num_groups=groups, topk_groups=keep, group_score=group_score, renormalize=renorm)
+    assert torch.equal(few[0], many[0][:200])
+    if score == "sigmoid":                           # (softmax sums its row in another order)
+        assert torch.equal(few[1][7:], many[1][7:200])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("topk", [9, 12, 15, 16])
+def test_near_ties_of_many_choices(topk):
+    E, m = 64, 2000
+    rng = np.random.default_rng(topk)
+    z = (rng.integers(-6, 7, (m, E)) / 4).astype(np.float32)
+    b = (rng.integers(0, 3, E) * 0.125 + rng.integers(-8, 9, E) * 2.0 ** -rng.integers(20, 27, E)).astype(np.float32)
+    b[::2] += rng.random(32).astype(np.float32)      # single pairs too
+    zt = torch.from_numpy(z).to(DEV)
+    for score in ("sigmoid", "softmax"):
+        check(zt, topk, torch.from_numpy(b), score)
+        check(zt, topk, torch.from_numpy(b), score, 8, 3, "top2")
+    z = (z.view(np.int32) + rng.integers(0, 3, z.shape).astype(np.int32) * (z != 0)).view(np.float32)
+    check(torch.from_numpy(z).to(DEV), topk, None, "sigmoid", 8, 3, "max")
+    check(torch.from_numpy(z).to(DEV), topk, None, "softmax")
