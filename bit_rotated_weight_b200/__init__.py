@@ -622,11 +622,17 @@ def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
     dtype, dims = _DTYPES.get(W.dtype), W.dim()
     if dtype is None or (dims != 2 and dims != 3) or not W.is_cuda:
         raise ValueError("W must be a CUDA float32/bfloat16/float16 tensor of shape [n][k] or [E][n][k]")
-    E, (n, k), device = W.shape[0] if dims == 3 else 1, W.shape[-2:], W.device
+    if dims == 3:
+        E, n, k = W.shape
+    else:
+        E, (n, k) = 1, W.shape
+    device = W.device
     W = W.contiguous()
-    out = Int8Weight(torch.empty(E, n, k, dtype=torch.int8, device=device),
-                     torch.empty(E, n, dtype=torch.float32, device=device), n, k, E)
-    rc = load_library().tq4_1s_int8_quantize(W.data_ptr(), dtype, out.c_struct(), _stream(device))
+    q = torch.empty(E, n, k, dtype=torch.int8, device=device)
+    wscale = torch.empty(E, n, dtype=torch.float32, device=device)
+    out = Int8Weight(q, wscale, n, k, E)
+    out._checked = st = _Int8Weight(n, k, E, 0, q.data_ptr(), wscale.data_ptr())
+    rc = load_library().tq4_1s_int8_quantize(W.data_ptr(), dtype, st, _stream(device))
     if rc:
         raise TQ4Error(rc, "int8_quantize")
     return out
@@ -634,12 +640,13 @@ def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
 
 def tq4_1s_int8_dequantize(w: Int8Weight) -> torch.Tensor:
     """The float32 weight [E][n][k] that w stands for."""
-    if _elsewhere(w.q):
-        with torch.cuda.device(w.q.device):
+    if _elsewhere(w._q):
+        with torch.cuda.device(w._q.device):
             return tq4_1s_int8_dequantize(w)
     st = w.c_struct()
-    out = torch.empty(w.num_experts, w.n, w.k, dtype=torch.float32, device=w.device)
-    rc = load_library().tq4_1s_int8_dequantize(st, out.data_ptr(), _stream(w.device))
+    device = w._q.device
+    out = torch.empty(w._num_experts, w._n, w._k, dtype=torch.float32, device=device)
+    rc = load_library().tq4_1s_int8_dequantize(st, out.data_ptr(), _stream(device))
     if rc:
         raise TQ4Error(rc, "int8_dequantize")
     return out

@@ -181,7 +181,8 @@ constexpr int kCountSlots = 2048;
 
 // The places of the block's rows: the slots with a smaller id, and those with
 // the same one earlier.  A warp a slot.
-__device__ __forceinline__ void count_rows(const RowsArgs& a, int64_t row0, int rows, int32_t* ids, int32_t (*s_at)[64]) {
+__device__ __forceinline__ void count_rows(const RowsArgs& a, int64_t row0, int rows, int32_t* ids,
+                                           int32_t (*s_at)[64]) {
   const int slots = static_cast<int>(a.rows) * a.topk, lane = threadIdx.x & 31;
   for (int p = threadIdx.x; p < slots; p += kRowThreads) ids[p] = __ldcg(a.ids + p);
   __syncthreads();

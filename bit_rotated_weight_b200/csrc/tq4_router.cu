@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsBlocks) router_rows_kern
             if (choice(j) < cut) continue;
             const float x = in_shared(z + g * sh.wide + j);
             // (without a bias every score has the same factor, which is left out)
-            const double from_top = SIGMOID ? static_cast<double>(x) : static_cast<double>(x) - static_cast<double>(largest);
+            const double from_top = static_cast<double>(x) - (SIGMOID ? 0.0 : static_cast<double>(largest));
             const Choice c = BIASED ? exact_choice<SIGMOID, true>(x, s_bias[g * (sh.wide + 4) + j], largest, inv64)
                                     : Choice{exact_score(from_top, SIGMOID), 0.0};
             most = fmax(most, c.part);
