@@ -580,12 +580,12 @@ def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | N
 class Int8Weight:
     """An int8 weight (stack): codes q int8 [E][n][k] and one float32 scale per row, wscale [E][n];
     the weight is wscale[e][i] * q[e][i][j].  The handle is fixed (make a new one for other tensors); the tensors'
-    contents may change."""
-    __slots__ = ("_q", "_wscale", "_n", "_k", "_num_experts", "_sizes", "_index", "_checked")
+    contents and storage may change."""
+    __slots__ = ("_q", "_wscale", "_n", "_k", "_num_experts", "_sizes", "_index", "_at", "_struct")
 
     def __init__(self, q: torch.Tensor, wscale: torch.Tensor, n: int, k: int, num_experts: int):
-        self._q, self._wscale, self._n, self._k, self._num_experts, self._checked = q, wscale, n, k, num_experts, None
-        self._sizes, self._index = (n, k, num_experts), q.get_device()
+        self._q, self._wscale, self._n, self._k, self._num_experts = q, wscale, n, k, num_experts
+        self._sizes, self._index, self._at, self._struct = (n, k, num_experts), q.get_device(), None, None
 
     q = property(lambda self: self._q)
     wscale = property(lambda self: self._wscale)
@@ -598,7 +598,10 @@ class Int8Weight:
         return f"Int8Weight(n={self._n}, k={self._k}, num_experts={self._num_experts}, device={self._q.device})"
 
     def c_struct(self) -> _Int8Weight:
-        if self._checked is None:
+        # checked and built once per place of the planes, which is looked at on every call
+        at = self._q.data_ptr(), self._wscale.data_ptr()
+        if at != self._at:
+            self._at = None
             q, s, E, n, k = self._q, self._wscale, self._num_experts, self._n, self._k
             if q.dtype != torch.int8 or q.numel() != E * n * k or not q.is_contiguous():
                 raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
@@ -606,8 +609,11 @@ class Int8Weight:
                 raise ValueError("Int8Weight.wscale must be a contiguous float32 tensor of num_experts * n scales")
             if q.device != s.device or not q.is_cuda:
                 raise ValueError("Int8Weight planes must lie on one CUDA device")
-            self._checked = _Int8Weight(n, k, E, 0, q.data_ptr(), s.data_ptr())
-        return self._checked
+            for t in (q, s):
+                if t.untyped_storage().nbytes() < (t.storage_offset() + t.numel()) * t.element_size():
+                    raise ValueError("an Int8Weight plane's storage has been freed or cut")
+            self._struct, self._index, self._at = _Int8Weight(n, k, E, 0, *at), q.get_device(), at
+        return self._struct
 
     @property
     def nbytes(self) -> int:
@@ -631,7 +637,8 @@ def tq4_1s_int8_quantize(W: torch.Tensor) -> Int8Weight:
     q = torch.empty(E, n, k, dtype=torch.int8, device=device)
     wscale = torch.empty(E, n, dtype=torch.float32, device=device)
     out = Int8Weight(q, wscale, n, k, E)
-    out._checked = st = _Int8Weight(n, k, E, 0, q.data_ptr(), wscale.data_ptr())
+    out._at = at = q.data_ptr(), wscale.data_ptr()
+    out._struct = st = _Int8Weight(n, k, E, 0, *at)
     rc = load_library().tq4_1s_int8_quantize(W.data_ptr(), dtype, st, _stream(device))
     if rc:
         raise TQ4Error(rc, "int8_quantize")
