@@ -565,7 +565,8 @@ def tq4_1s_router_scored(logits: torch.Tensor, topk: int, bias: torch.Tensor | N
             raise ValueError("bias must be a float32 [E] tensor on the logits' device")
         bias = bias.contiguous()
         pb = bias.data_ptr()
-    cfg = _router_struct(E, topk, score, num_groups, topk_groups, group_score, renormalize, scale)
+    # (kept by values: a tensor would be its own key, whatever it holds later; 0.0 and -0.0 are one key)
+    cfg = _router_struct(E, topk, score, num_groups, topk_groups, group_score, bool(renormalize), float(scale) + 0.0)
     device = logits.device
     # (sizes as arguments: a tuple costs half a microsecond more)
     ids = torch.empty(m, max(topk, 0), dtype=torch.int32, device=device)
