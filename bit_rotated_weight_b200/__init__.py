@@ -313,6 +313,17 @@ def tq4_1s_linear(x: torch.Tensor, w: Packed, out: torch.Tensor | None = None,
     return out
 
 
+def _ids32(ids: torch.Tensor, num_experts: int) -> torch.Tensor:
+    """Expert ids as int32.  Wider ones outside [0, num_experts) stay outside (2**32 + 3 is not expert 3)."""
+    if ids.dtype == torch.int32:   # (a conversion to its own type costs half a microsecond)
+        return ids
+    if ids.dtype == torch.uint64:   # (from 2**63 on: negative)
+        ids = ids.view(torch.int64)
+    if ids.dtype == torch.int64:
+        ids = ids.clamp(-1, num_experts)
+    return ids.to(torch.int32)
+
+
 def tq4_1s_moe_workspace(m: int, topk: int, up: Packed, down: Packed) -> int:
     u, d = up.c_struct(), down.c_struct()
     return load_library().tq4_1s_moe_workspace(m, topk, ctypes.byref(u), ctypes.byref(d))
@@ -324,7 +335,7 @@ def tq4_1s_moe(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, up
     if x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
         raise ValueError("x must be a CUDA bfloat16 [m][H] tensor")
     x = x.contiguous()
-    topk_ids = topk_ids.to(torch.int32).contiguous()
+    topk_ids = _ids32(topk_ids, up.num_experts).contiguous()
     topk_w = topk_w.to(torch.float32).contiguous()
     m, topk = topk_ids.shape
     if out is None:
@@ -376,7 +387,7 @@ def tq4_1s_router_topk(logits: torch.Tensor, topk: int):
 
 def tq4_1s_moe_route(topk_ids: torch.Tensor, num_experts: int):
     """(offsets [E+1], pairs [m*topk]) -- the routing step of tq4_1s_moe."""
-    topk_ids = topk_ids.to(torch.int32).contiguous()
+    topk_ids = _ids32(topk_ids, num_experts).contiguous()
     m, topk = topk_ids.shape
     offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=topk_ids.device)
     pairs = torch.empty(m * topk, dtype=torch.int32, device=topk_ids.device)
@@ -745,8 +756,7 @@ def tq4_1s_moe_int8(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tenso
     if not (topk_ids.get_device() == topk_w.get_device() == up._index == down._index == index):
         raise ValueError("x, the routing and the weights must lie on one device")
     x = x.contiguous()
-    if topk_ids.dtype != torch.int32:   # (a conversion to its own type costs half a microsecond)
-        topk_ids = topk_ids.to(torch.int32)
+    topk_ids = _ids32(topk_ids, up._num_experts)
     if topk_w.dtype != torch.float32:
         topk_w = topk_w.to(torch.float32)
     topk_ids, topk_w = topk_ids.contiguous(), topk_w.contiguous()
