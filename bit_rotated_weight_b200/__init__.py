@@ -615,10 +615,14 @@ class Int8Weight:
         if at != self._at:
             self._at = None
             q, s, E, n, k = self._q, self._wscale, self._num_experts, self._n, self._k
-            if q.dtype != torch.int8 or q.numel() != E * n * k or not q.is_contiguous():
-                raise ValueError("Int8Weight.q must be a contiguous int8 tensor of num_experts * n * k codes")
-            if s.dtype != torch.float32 or s.numel() != E * n or not s.is_contiguous():
-                raise ValueError("Int8Weight.wscale must be a contiguous float32 tensor of num_experts * n scales")
+            # (leading dimensions may be merged; a [k][n] plane has as many codes, but they are another weight's)
+            if (q.dtype != torch.int8 or q.shape not in ((E, n, k), (E * n, k), (E * n * k,))
+                    or not q.is_contiguous()):
+                raise ValueError(f"Int8Weight.q must be a contiguous int8 [{E}][{n}][{k}] tensor, not {tuple(q.shape)}")
+            if (s.dtype != torch.float32 or s.shape not in ((E, n), (E * n,), (E, n, 1), (E * n, 1))
+                    or not s.is_contiguous()):
+                raise ValueError(f"Int8Weight.wscale must be a contiguous float32 [{E}][{n}] tensor, not "
+                                 f"{tuple(s.shape)}")
             if q.device != s.device or not q.is_cuda:
                 raise ValueError("Int8Weight planes must lie on one CUDA device")
             for t in (q, s):

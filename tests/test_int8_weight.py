@@ -74,6 +74,27 @@ def test_handle_refuses_planes_whose_storage_is_gone():
     assert w.c_struct().q == 32768 + 64
 
 
+def test_handle_takes_planes_of_its_shape_only():
+    E, n, k = 2, 8, 32
+
+    def handle(qs, ss):
+        return tq.Int8Weight(Plane(qs, torch.int8, 4096), Plane(ss, torch.float32, 65536), n, k, E).c_struct()
+
+    for qs in ((E, n, k), (E * n, k), (E * n * k,)):
+        for ss in ((E, n), (E * n,), (E, n, 1), (E * n, 1)):
+            assert handle(qs, ss).q == 4096
+    for qs in ((E, k, n), (k, E * n), (n, E, k), (1, E * n, k), (E, n, k, 1), (E, n, k - 1), (E * k, n)):
+        with pytest.raises(ValueError, match="Int8Weight.q"):
+            handle(qs, (E, n))
+    for ss in ((n, E), (1, E * n), (E, 1, n), (E, n + 1)):
+        with pytest.raises(ValueError, match="Int8Weight.wscale"):
+            handle((E, n, k), ss)
+    one = tq.Int8Weight(Plane((n, k), torch.int8, 4096), Plane((n,), torch.float32, 65536), n, k, 1)
+    assert one.c_struct().n == n
+    with pytest.raises(ValueError, match="Int8Weight.q"):
+        tq.Int8Weight(Plane((k, n), torch.int8, 4096), Plane((n,), torch.float32, 65536), n, k, 1).c_struct()
+
+
 # ------------------------------------------------------------------ on the GPU
 def small(seed, E=1, n=64, k=96):
     return tq.tq4_1s_int8_quantize(torch.randn(E, n, k, generator=torch.Generator().manual_seed(seed)).to(DEV))
@@ -119,3 +140,14 @@ def test_experts_moved_out_and_back():
     assert torch.equal(tq.tq4_1s_moe_int8(x, ids, tw, up, down), want)
     assert bool((taken == 7).all())
     assert np.array_equal(up.q.cpu().numpy(), host.numpy())
+
+
+@pytest.mark.gpu
+def test_a_transposed_plane_is_refused():
+    w = small(6)
+    x = torch.ones(3, 96, device=DEV)
+    want = tq.tq4_1s_linear_int8(x, w)
+    turned = tq.Int8Weight(w.q[0].t().contiguous(), w.wscale, 64, 96, 1)
+    with pytest.raises(ValueError, match="Int8Weight.q"):
+        tq.tq4_1s_linear_int8(x, turned)
+    assert torch.equal(tq.tq4_1s_linear_int8(x, tq.Int8Weight(w.q[0], w.wscale[0], 64, 96, 1)), want)
