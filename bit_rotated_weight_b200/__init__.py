@@ -606,6 +606,9 @@ class Int8Weight:
     num_experts = property(lambda self: self._num_experts)
     device = property(lambda self: self._q.device)
 
+    def __reduce__(self):   # (the struct holds addresses: a copy makes its own)
+        return type(self), (self._q, self._wscale, self._n, self._k, self._num_experts)
+
     def __repr__(self) -> str:
         return f"Int8Weight(n={self._n}, k={self._k}, num_experts={self._num_experts}, device={self._q.device})"
 

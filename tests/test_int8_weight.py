@@ -1,4 +1,7 @@
 """The handle of an int8 weight: what it tells the kernels has to be what its planes hold now."""
+import copy
+import pickle
+
 import numpy as np
 import pytest
 import torch
@@ -95,6 +98,19 @@ def test_handle_takes_planes_of_its_shape_only():
         tq.Int8Weight(Plane((k, n), torch.int8, 4096), Plane((n,), torch.float32, 65536), n, k, 1).c_struct()
 
 
+def test_a_handle_that_was_used_can_be_copied_and_pickled():
+    q, s = planes()
+    w = tq.Int8Weight(q, s, 8, 32, 2)
+    w.c_struct()
+    shared, own, loaded = copy.copy(w), copy.deepcopy(w), pickle.loads(pickle.dumps(w))
+    assert shared.q is q and own.q is not q and loaded.q is not q
+    for v in (shared, own, loaded):
+        assert (v.n, v.k, v.num_experts, v.nbytes) == (8, 32, 2, w.nbytes)
+    own.q.at, loaded.wscale.at = 8192, 1 << 20             # (planes of their own, elsewhere)
+    assert (own.c_struct().q, loaded.c_struct().wscale) == (8192, 1 << 20)
+    assert (w.c_struct().q, w.c_struct().wscale) == (4096, 65536)
+
+
 # ------------------------------------------------------------------ on the GPU
 def small(seed, E=1, n=64, k=96):
     return tq.tq4_1s_int8_quantize(torch.randn(E, n, k, generator=torch.Generator().manual_seed(seed)).to(DEV))
@@ -151,3 +167,13 @@ def test_a_transposed_plane_is_refused():
     with pytest.raises(ValueError, match="Int8Weight.q"):
         tq.tq4_1s_linear_int8(x, turned)
     assert torch.equal(tq.tq4_1s_linear_int8(x, tq.Int8Weight(w.q[0], w.wscale[0], 64, 96, 1)), want)
+
+
+@pytest.mark.gpu
+def test_copies_of_a_used_handle_multiply_alike():
+    w, x = small(7), torch.ones(3, 96, device=DEV)
+    want = tq.tq4_1s_linear_int8(x, w)
+    own, loaded = copy.deepcopy(w), pickle.loads(pickle.dumps(w))
+    w.q.zero_()
+    for v in (own, loaded):
+        assert torch.equal(tq.tq4_1s_linear_int8(x, v), want)
