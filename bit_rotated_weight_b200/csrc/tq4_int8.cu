@@ -680,6 +680,7 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   if (stream_rows) {
     if (!encode_i8_map(&tw, w->q, w->num_experts, w->n, w->k, 128)) return TQ_ERR_CUDA;
     Int8StreamArgs a{};
+    a.test_withhold = withhold_arrival_hook() ? 1 : 0;
     a.n = static_cast<int32_t>(w->n);
     a.k = static_cast<int32_t>(w->k);
     a.m = static_cast<int32_t>(m);
@@ -708,6 +709,7 @@ TQ_API int tq4_1s_linear_int8(const void* x, int dtype, int64_t m, int64_t ldx, 
   r.scale = reinterpret_cast<float*>(base + L.xscale);
   if (launch_rows(dtype, r, st) != cudaSuccess) return TQ_ERR_CUDA;
   Int8GemmArgs a{};
+  a.test_withhold = withhold_arrival_hook() ? 1 : 0;
   a.n = static_cast<int32_t>(w->n);
   a.m = static_cast<int32_t>(m);
   a.row_tiles = static_cast<int32_t>(p.row_tiles);
@@ -792,6 +794,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   const int64_t tiles_up = L.maxseg * rt_up, tiles_dn = L.maxseg * rt_dn;
   if (stream_rows) {
     Int8StreamArgs s{};
+    s.test_withhold = withhold_arrival_hook() ? 1 : 0;
     s.n = static_cast<int32_t>(I);
     s.k = static_cast<int32_t>(H);
     s.row_tiles = static_cast<int32_t>(rt_up);
@@ -828,6 +831,7 @@ TQ_API int tq4_1s_moe_int8(const void* x, int dtype, int64_t m, const int32_t* t
   } else {
     if (launch_rows(dtype, r, st, counted ? &sa : nullptr) != cudaSuccess) return TQ_ERR_CUDA;
     Int8GemmArgs a{};
+    a.test_withhold = withhold_arrival_hook() ? 1 : 0;
     a.n = static_cast<int32_t>(I);
     a.row_tiles = static_cast<int32_t>(rt_up);
     a.ksteps = static_cast<int32_t>((H + 127) / 128);

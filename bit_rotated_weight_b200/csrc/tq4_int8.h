@@ -21,6 +21,7 @@ struct Int8GemmArgs {
   const int32_t* pairs;     // down: flat slot of each sorted row
   const float* row_w;       // down: router weight of each sorted row
   void* y;                  // dense: y [m][n]; up: h bf16 [rows][n]; down: fp32 [slots][n]
+  int32_t test_withhold;    // test hook: a CTA's first tile is never reported (the bounded waits for it run out)
 };
 
 // A tensor map over int8 [experts][rows][k] (3-D), or [rows][k] where experts
@@ -54,6 +55,7 @@ struct Int8StreamArgs {
   int32_t slots, experts;   // (slots <= kStreamSlots)
   const float* wscale;
   void* y;                  // as Int8GemmArgs
+  int32_t test_withhold;    // test hook: a quantizer warp never reports its first codes
 };
 constexpr int kStreamSlots = 128;
 // Whether rows of k elements fit (their codes stay in shared memory).

@@ -50,6 +50,7 @@ struct Shared {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  int filled;                                       // copies sent to the ring
   int epi_ok[2];
   alignas(16) float sx[2][NT < 32 ? 32 : NT];       // the tile's token scales,
   alignas(16) float tw[2][NT < 32 ? 32 : NT];       // router weights and
@@ -268,12 +269,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           }
         }
       }
-      if (*abortp)   // let the copies in flight land before the CTA leaves
-        for (int i = 0; i < min(li, S::kStages); ++i) {
-          s = s == 0 ? S::kStages - 1 : s - 1;
-          if (s == S::kStages - 1) ph ^= 1u;
-          int8_drain_wait(&sh.full[s], ph);
-        }
+      sh.filled = li;
     }
   } else if (warp == 1) {
     // The whole warp walks, one elected lane issues: values that are the same
@@ -306,7 +302,7 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
           ph ^= 1u;
         }
       }
-      if (ok && elect_one()) mma_commit(&sh.dfull[db]);
+      if (ok && !(a.test_withhold && ti == 0) && elect_one()) mma_commit(&sh.dfull[db]);
       __syncwarp();
       ++ti;
     }
@@ -376,6 +372,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, S::kTmemCols);
+  // Where a wait ran out, copies may be in flight.  (Not before here: a role
+  // may give up after the last copy was sent.)
+  if (threadIdx.x == 0 && *abortp) int8_land_copies(sh.full, S::kStages, sh.filled);
 }
 
 // ------------------------------------------------------------------ pairs

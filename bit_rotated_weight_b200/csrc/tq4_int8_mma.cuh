@@ -110,4 +110,11 @@ __device__ __forceinline__ void int8_drain_wait(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// Waits for a ring's copies in flight: `filled` were sent, the last `stages` of
+// them may not have landed.
+__device__ __forceinline__ void int8_land_copies(uint64_t* full, int stages, int filled) {
+#pragma unroll 1
+  for (int i = max(0, filled - stages); i < filled; ++i) int8_drain_wait(&full[i % stages], (i / stages) & 1);
+}
+
 }  // namespace tq4

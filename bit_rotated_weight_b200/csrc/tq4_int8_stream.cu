@@ -64,6 +64,7 @@ struct Shared {
   uint64_t maxima, sums;                   // cluster form: what the other CTAs send has arrived
   uint32_t tmem_base;
   int abort_flag;
+  int filled;                              // copies sent to the ring
   uint32_t top[kTok];                      // largest |x| of each token, as bits (persistent form)
   uint32_t tops[kMaxParts][kTok];          // [CTA][row, or warp of a row] (cluster form)
   float sx[kTok], tw[kTok];
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int filled = 0;   // stages that a copy was sent to, and the phase of the last
+      int filled = 0;   // copies sent
       bool ok = true;
 #pragma unroll 1
       for (; ok && w.left > 0; w.next()) {
@@ -317,17 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++filled;
         }
       }
-      if (*abortp) {   // let the copies in flight land before the CTA leaves
-        const int n = min(filled, stages);
-        for (int i = 0; i < n; ++i) {
-          pos.at -= 1;
-          if (pos.at < 0) {
-            pos.at += stages;
-            pos.phase ^= 1u;
-          }
-          int8_drain_wait(&sh.full[pos.at], pos.phase);
-        }
-      }
+      sh.filled = filled;
     }
     __syncwarp();
   } else if (warp <= kIssuers) {
@@ -474,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(2, kQuantThreads);   // every thread has read its row's maximum
         if (q < kTok) sh.top[q] = 0;
       }
-      mbar_arrive(&sh.bfull);
+      if (!(a.test_withhold && warp == 8 && turn == 0)) mbar_arrive(&sh.bfull);
     }
   } else {
     // ---- epilogue
@@ -575,6 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(sh.tmem_base, 2 * kAcc);
+  // Where a wait ran out, copies may be in flight.  (Not before here: a role
+  // may give up after the last copy was sent.)
+  if (threadIdx.x == 0 && *abortp) int8_land_copies(sh.full, stages, sh.filled);
 }
 
 template <typename T>

@@ -1,0 +1,144 @@
+"""How the int8 kernels end when a wait runs out, on the CPU.
+
+No CTA may leave while something is still on its way into its shared memory: copies of its own, and what other CTAs
+send.  The models run the roles in random order; a role gives up at a random moment, as a wait that runs out does, and the
+others learn of it at their next wait that does not pass.
+
+On the GPU a hook withholds one report and shortens the limit of every wait to 2 ms: the call has to end, to report
+TQ_DEV_TIMEOUT, and to leave the context and the next calls as they were."""
+import os
+import random
+import time
+
+import pytest
+import torch
+
+import bit_rotated_weight_b200 as tq
+
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+CSRC = os.path.join(os.path.dirname(__file__), "..", "bit_rotated_weight_b200", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+# ------------------------------------------------------------------ copies of the CTA itself
+def one_cta(stages, issuers, total, seed, at_end):
+    """Copies in flight when the CTA leaves.  `at_end`: where someone gave up, the last copies are waited for when every
+    role has ended; else by the producer, when it has sent the last."""
+    rng = random.Random(seed)
+    give_up = rng.randrange(4 * total)                     # events until the epilogue gives up
+    full, empty = [0] * stages, [0] * stages               # completed phases
+    flying, pending = [], []
+    sent, aborted, wait_for = 0, False, None
+    turn = list(range(issuers))                            # each issuer's next fill
+    producing, left = True, list(range(issuers))
+    events = 0
+    while True:
+        events += 1
+        assert events < 100000
+        aborted = aborted or events >= give_up
+        act = rng.randrange(issuers + 3)
+        if act == 0 and flying and rng.random() < 0.3:
+            full[flying.pop(rng.randrange(len(flying))) % stages] += 1
+        elif act == 1 and pending:
+            empty[pending.pop(0)] += 1
+        elif act == 2 and producing:
+            if wait_for is None:
+                free = sent < stages or empty[sent % stages] >= sent // stages
+                if sent == total or (not free and aborted):
+                    wait_for = list(range(max(0, sent - stages), sent)) if aborted and not at_end else []
+                elif free:
+                    flying.append(sent)
+                    sent += 1
+            else:
+                producing = not all(full[li % stages] > li // stages for li in wait_for)
+        elif act >= 3 and act - 3 in left:
+            me = act - 3
+            if turn[me] >= total:
+                left.remove(me)
+            elif full[turn[me] % stages] > turn[me] // stages:
+                pending.append(turn[me] % stages)
+                turn[me] += issuers
+            elif aborted:
+                left.remove(me)
+        if aborted and not producing and not left and not (
+                at_end and any(full[li % stages] <= li // stages for li in range(max(0, sent - stages), sent))):
+            return flying
+
+
+@pytest.mark.parametrize("name,issuers", [("tq4_int8_stream.cu", 3), ("tq4_int8_gemm.cu", 1)])
+@pytest.mark.parametrize("stages,total", [(3, 3), (3, 2), (6, 5), (6, 21), (12, 40)])
+def test_own_copies_have_landed(name, issuers, stages, total):
+    # where the source waits for them: behind the block's last barrier?
+    kernel = source(name).split("// ---", 1)[0] if "gemm" in name else source(name)
+    waits = max(kernel.rfind("int8_land_copies("), kernel.rfind("int8_drain_wait(&sh.full["))
+    for seed in range(200):
+        assert one_cta(stages, issuers, total, seed, waits > kernel.rindex("  __syncthreads();")) == []
+
+
+def test_the_model_sees_copies_left_behind():
+    assert any(one_cta(6, 1, 5, seed, False) for seed in range(200))
+
+
+# ------------------------------------------------------------------ on the GPU
+@pytest.fixture
+def hooks():
+    tq.tq4_1s_get_status()
+    yield
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_FAIL_NEXT_CALLS, 0)
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WITHHOLD_ARRIVAL, 0)
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WAIT_NS, 0)
+
+
+def runs_out(call):
+    """`call` with a report withheld, between two that are whole."""
+    want = call()
+    torch.cuda.synchronize()
+    assert tq.tq4_1s_get_status() == 0
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WAIT_NS, 2_000_000)
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WITHHOLD_ARRIVAL, 1)
+    t0 = time.perf_counter()
+    call()
+    torch.cuda.synchronize()
+    elapsed = time.perf_counter() - t0
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WITHHOLD_ARRIVAL, 0)
+    tq.tq4_1s_debug_hook(tq.TQ_HOOK_WAIT_NS, 0)
+    assert tq.tq4_1s_get_status() & tq.TQ_DEV_TIMEOUT
+    assert elapsed < 1.0
+    for _ in range(3):
+        assert torch.equal(call().view(torch.int16), want.view(torch.int16))
+    assert tq.tq4_1s_get_status() == 0
+
+
+def linear(m, n, k):
+    g = torch.Generator().manual_seed(m + n + k)
+    w = tq.tq4_1s_int8_quantize(torch.randn(n, k, generator=g).to(DEV))
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16).to(DEV)
+    return lambda: tq.tq4_1s_linear_int8(x, w)
+
+
+def moe(m, E, topk, H, I):
+    g = torch.Generator().manual_seed(m + E)
+    up = tq.tq4_1s_int8_quantize(torch.randn(E, I, H, generator=g).to(DEV))
+    down = tq.tq4_1s_int8_quantize(torch.randn(E, H, I, generator=g).to(DEV))
+    x = (0.1 * torch.randn(m, H, generator=g)).to(torch.bfloat16).to(DEV)
+    ids = torch.randn(m, E, generator=g).argsort(1)[:, :topk].to(torch.int32).to(DEV)
+    tw = torch.rand(m, topk, generator=g).to(DEV)
+    return lambda: tq.tq4_1s_moe_int8(x, ids, tw, up, down)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(9, 40000, 256), (3, 20000, 4096), (40, 300, 64), (300, 4096, 1024), (100, 40000, 512)])
+def test_linear_winds_down(hooks, m, n, k):
+    # few tokens, many row tiles a block; one tile a block, and several
+    runs_out(linear(m, n, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,E,topk,H,I", [(2, 16, 4, 256, 128), (300, 8, 2, 512, 288)])
+def test_moe_winds_down(hooks, m, E, topk, H, I):
+    # slots sorted in the product, a segment a block; grouped tiles
+    runs_out(moe(m, E, topk, H, I))
