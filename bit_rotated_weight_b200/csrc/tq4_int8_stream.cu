@@ -65,6 +65,7 @@ struct Shared {
   uint32_t tmem_base;
   int abort_flag;
   int filled;                              // copies sent to the ring
+  int quit;                                // a quantizer's wait ran out
   uint32_t top[kTok];                      // largest |x| of each token, as bits (persistent form)
   uint32_t tops[kMaxParts][kTok];          // [CTA][row, or warp of a row] (cluster form)
   float sx[kTok], tw[kTok];
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (lane == 18) {
       mbar_init(&sh.bfull, kQuantThreads);
       mbar_init(&sh.bempty, kIssuers + kEpilogue);   // (the epilogue reads the scales)
-      sh.abort_flag = 0;
+      sh.abort_flag = sh.quit = 0;
       for (int i = 0; i < kIssuers; ++i) mbar_init(&sh.drained[i], 1);
       if (CLUSTER) {
         const int tpr = threads_per_row(a.m);   // a word per row and warp of it from every CTA
@@ -378,9 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- the tokens' codes
     const int q = threadIdx.x - 256;
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
-    bool ok = true;
+    // Where a wait ran out they stop together, before they report the segment:
+    // the barrier counts one report a thread and phase, and waits for what it
+    // guards alone keep a report out of the phase before.
+    bool ok = true, go = true;
 #pragma unroll 1
-    for (int32_t s = seg0, n = (w.row_tile + w.left + a.row_tiles - 1) / a.row_tiles; n > 0 && w.left > 0; ++s, --n) {
+    for (int32_t s = seg0, n = (w.row_tile + w.left + a.row_tiles - 1) / a.row_tiles; go && n > 0 && w.left > 0;
+         ++s, --n) {
       const int turn = s - seg0;
       const int4 sg = segment(s);
       const int tpr = threads_per_row(sg.z);
@@ -432,7 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         if (leader) atomicMax(&sh.top[r], top);
+        if (!ok) sh.quit = 1;
         named_bar_sync(2, kQuantThreads);
+        go = *const_cast<volatile int*>(&sh.quit) == 0;   // (the same for all: written before the barrier only)
         if (live) row_top = *reinterpret_cast<volatile uint32_t*>(&sh.top[r]);
       }
       const RowUnit u(Vec<T>::top_f32(row_top));
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(2, kQuantThreads);   // every thread has read its row's maximum
         if (q < kTok) sh.top[q] = 0;
       }
-      if (!(a.test_withhold && warp == 8 && turn == 0)) mbar_arrive(&sh.bfull);
+      if (go && !(a.test_withhold && warp == 8 && turn == 0)) mbar_arrive(&sh.bfull);
     }
   } else {
     // ---- epilogue

@@ -1,8 +1,8 @@
 """How the int8 kernels end when a wait runs out, on the CPU.
 
 No CTA may leave while something is still on its way into its shared memory: copies of its own, and what other CTAs
-send.  The models run the roles in random order; a role gives up at a random moment, as a wait that runs out does, and the
-others learn of it at their next wait that does not pass.
+send.  The models run the roles in random order; a role gives up at a random moment, as a wait that runs out does, and
+the others learn of it at their next wait that does not pass.
 
 On the GPU a hook withholds one report and shortens the limit of every wait to 2 ms: the call has to end, to report
 TQ_DEV_TIMEOUT, and to leave the context and the next calls as they were."""
@@ -83,6 +83,102 @@ def test_the_model_sees_copies_left_behind():
     assert any(one_cta(6, 1, 5, seed, False) for seed in range(200))
 
 
+# ------------------------------------------------------------------ the tokens' codes
+class Counted:
+    """A barrier of so many arrivals a phase.  One operation of several threads must not run past the end of a phase."""
+
+    def __init__(self, count):
+        self.count, self.pending, self.phase = count, count, 0
+
+    def arrive(self, n=1):
+        assert n <= self.pending, f"{n} arrivals at a phase with {self.pending} pending"
+        self.pending -= n
+        if self.pending == 0:
+            self.phase, self.pending = self.phase + 1, self.count
+
+
+def few_tokens(segments, withheld, seed, stop):
+    """The roles that share the tokens' codes: 8 warps of quantizers (`withheld` threads of the first do not report the
+    first segment), 3 issuers and 4 warps of the epilogue.  `stop`: quantizers whose wait ran out report no more."""
+    rng = random.Random(seed)
+    bfull, bempty, dfull = Counted(256), Counted(3 + 128), [Counted(3) for _ in range(segments)]
+    give_up = rng.randrange(200, 800)                      # waits that began with the call run out from here on
+    aborted = False
+    turn = {("q", i): 0 for i in range(8)}
+    turn.update({("i", i): 0 for i in range(3)})
+    turn.update({("e", i): 0 for i in range(4)})
+    inside = {("e", i): False for i in range(4)}           # has passed the wait for the codes
+    at = {("q", i): "wait" for i in range(8)}              # for the last segment's readers, then the named barriers
+    quit_ = False
+    running = set(turn)
+    for event in range(200000):
+        if not running:
+            return
+        r = rng.choice(sorted(running))
+        kind, t = r[0], turn[r]
+        late = aborted or (event > give_up and rng.random() < 0.1)
+        if t == segments:
+            running.discard(r)
+        elif kind == "q":
+            if at[r] == "wait":
+                free = bempty.phase >= t
+                if free or late:
+                    aborted |= not free
+                    quit_ |= stop and not free
+                    at[r] = "barrier"
+                if all(v == "barrier" for v in at.values()):
+                    at = dict.fromkeys(at, "left" if quit_ else "report")
+            elif at[r] == "left":
+                running.discard(r)
+            elif at[r] == "report":
+                n = 32 - (withheld if r[1] == 0 and t == 0 else 0)
+                if n:
+                    bfull.arrive(n)
+                turn[r], at[r] = t + 1, "wait"
+        elif kind == "i":
+            if bfull.phase > t:
+                dfull[t].arrive()
+                bempty.arrive()
+                turn[r] += 1
+            elif late:
+                aborted = True
+                running.discard(r)
+        else:
+            if not inside[r] and bfull.phase > t:
+                inside[r] = True
+            elif inside[r] and dfull[t].phase:
+                bempty.arrive(32)
+                inside[r] = False
+                turn[r] += 1
+            elif late:
+                aborted = True
+                running.discard(r)
+    raise AssertionError("stuck")
+
+
+@pytest.mark.parametrize("withheld", [0, 1, 32])
+@pytest.mark.parametrize("segments", [1, 2, 5])
+def test_reports_stay_in_their_phase(segments, withheld):
+    # do the quantizers leave their loop where a wait ran out?
+    loop = source("tq4_int8_stream.cu").split("for (int32_t s = seg0", 1)[1].split("{", 1)[0]
+    for seed in range(300):
+        few_tokens(segments, withheld, seed, "go &&" in loop)
+
+
+def test_the_model_sees_reports_that_run_over():
+    def overruns(withheld):
+        n = 0
+        for seed in range(300):
+            try:
+                few_tokens(3, withheld, seed, False)
+            except AssertionError as e:
+                assert "pending" in str(e)
+                n += 1
+        return n
+
+    assert overruns(1) > 0 and overruns(32) == 0
+
+
 # ------------------------------------------------------------------ on the GPU
 @pytest.fixture
 def hooks():
@@ -131,14 +227,15 @@ def moe(m, E, topk, H, I):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m,n,k", [(9, 40000, 256), (3, 20000, 4096), (40, 300, 64), (300, 4096, 1024), (100, 40000, 512)])
+@pytest.mark.parametrize("m,n,k", [(9, 40000, 256), (3, 20000, 4096), (40, 300, 64), (300, 4096, 1024),
+                                   (100, 40000, 512)])
 def test_linear_winds_down(hooks, m, n, k):
     # few tokens, many row tiles a block; one tile a block, and several
     runs_out(linear(m, n, k))
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("m,E,topk,H,I", [(2, 16, 4, 256, 128), (300, 8, 2, 512, 288)])
+@pytest.mark.parametrize("m,E,topk,H,I", [(2, 16, 4, 256, 128), (90, 300, 3, 160, 96), (300, 8, 2, 512, 288)])
 def test_moe_winds_down(hooks, m, E, topk, H, I):
-    # slots sorted in the product, a segment a block; grouped tiles
+    # slots sorted in the product, a segment a block; segments from a kernel of their own, several a block; tiles
     runs_out(moe(m, E, topk, H, I))
