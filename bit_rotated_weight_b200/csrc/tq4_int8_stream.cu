@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              in_cta(&sh.tops[rank][at], p)),
                          "r"(top), "r"(in_cta(&sh.maxima, p))
                          : "memory");
-        if (!mbar_wait(&sh.maxima, 0, abortp)) ok = false;
+        mbar_wait_cluster(&sh.maxima, 0, abortp);   // (where it runs out the epilogue stores nothing)
         if (live) {
           const int n_at = tpr > 32 ? tpr / 32 : 1, at0 = tpr > 32 ? r * n_at : r;
           for (int p = 0; p < a.parts; ++p)
@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(2, kQuantThreads);   // every thread has read its row's maximum
         if (q < kTok) sh.top[q] = 0;
       }
-      if (go && !(a.test_withhold && warp == 8 && turn == 0)) mbar_arrive(&sh.bfull);
+      if (go && !(a.test_withhold && warp == 8 && turn == 0 && rank == 0)) mbar_arrive(&sh.bfull);
+      if (CLUSTER) cluster_arrive_relaxed();
     }
   } else {
     // ---- epilogue
@@ -524,10 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     to + j * 4),
                 "r"(acc[j]), "r"(acc[j + 1]), "r"(acc[j + 2]), "r"(acc[j + 3]), "r"(bar)
                 : "memory");
+        cluster_arrive_relaxed();   // (these are the last)
         int never = 0;   // (no giving up for an abort: others' stores may be on their way here)
-        mbar_wait(&sh.sums, 0, &never);
+        const bool got = mbar_wait_cluster(&sh.sums, 0, &never);
+        if (!got) *abortp = 1;
         const int row_base = w.row_tile * kRows + rank * per;
-        for (int i = t; i < per * (kTok / 4); i += kEpilogue) {
+        for (int i = ok && got && !*abortp ? t : INT32_MAX; i < per * (kTok / 4); i += kEpilogue) {
           const int rl = i % per, j0 = i / per * 4, out_row = row_base + rl;
           if (out_row >= a.n || j0 >= sg.z) continue;
           int4 sum = make_int4(0, 0, 0, 0);
@@ -568,14 +571,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  if (CLUSTER && warp < 4) cluster_wait();
+  if (CLUSTER) {
+    // No CTA leaves before every other has sent what it sends: one whose wait
+    // ran out would be written to after its end.
+    if (warp < 4) {
+      cluster_wait();
+      cluster_arrive_relaxed();
+    }
+    cluster_wait();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(sh.tmem_base, 2 * kAcc);
-  // Where a wait ran out, copies may be in flight.  (Not before here: a role
-  // may give up after the last copy was sent.)
-  if (threadIdx.x == 0 && *abortp) int8_land_copies(sh.full, stages, sh.filled);
+  // Where a wait ran out, copies may be in flight, and what other CTAs sent.
+  // (Not before here: a role may give up after the last copy was sent.)
+  if (threadIdx.x == 0 && *abortp) {
+    int8_land_copies(sh.full, stages, sh.filled);
+    if (CLUSTER) {
+      int8_drain_wait(&sh.maxima, 0);
+      int8_drain_wait(&sh.sums, 0);
+    }
+  }
 }
 
 template <typename T>

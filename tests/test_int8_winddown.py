@@ -179,6 +179,63 @@ def test_the_model_sees_reports_that_run_over():
     assert overruns(1) > 0 and overruns(32) == 0
 
 
+# ------------------------------------------------------------------ what other CTAs send
+def cluster(parts, seed, barrier):
+    """CTAs that exchange maxima, then sums, by stores that land some time after they are sent.  A CTA may be slow, and
+    its waits run out.  None may be written to after it left.  `barrier`: the CTAs end together, and one whose wait ran
+    out then waits for what was sent."""
+    rng = random.Random(seed)
+    speed = [rng.choice([1.0, 0.3, 0.02]) for _ in range(parts)]
+    patience = rng.randrange(20, 400)
+    step = ["send maxima"] * parts
+    since = [0] * parts
+    landed = [{"maxima": 0, "sums": 0} for _ in range(parts)]
+    sent = [{"maxima": 0, "sums": 0} for _ in range(parts)]       # to this CTA
+    flying, gone, gave_up = [], set(), set()
+    for now in range(1000000):
+        if len(gone) == parts and not flying:
+            return gave_up
+        if flying and rng.random() < 0.4:
+            to, what = flying.pop(rng.randrange(len(flying)))
+            assert to not in gone, "written to after its end"
+            landed[to][what] += 1
+        c = rng.randrange(parts)
+        if c in gone or rng.random() > speed[c]:
+            continue
+        verb, _, what = step[c].partition(" ")
+        if verb == "send":
+            for to in range(parts):
+                assert to not in gone, "written to after its end"
+                flying.append((to, what))
+                sent[to][what] += 1
+            step[c], since[c] = "await " + what, now
+        elif verb == "await":
+            if landed[c][what] < parts:
+                if now - since[c] < patience:
+                    continue
+                gave_up.add(c)
+            step[c] = "send sums" if what == "maxima" else "end"
+        elif not barrier:
+            gone.add(c)
+        elif all(s == "end" for i, s in enumerate(step)) and (c not in gave_up or landed[c] == sent[c]):
+            gone.add(c)
+    raise AssertionError("stuck")
+
+
+@pytest.mark.parametrize("parts", [2, 4, 8])
+def test_a_cluster_ends_together(parts):
+    tail = source("tq4_int8_stream.cu")
+    tail = tail[tail.rindex("mbar_arrive(&sh.bempty);"):tail.rindex("tmem_dealloc(")]
+    runs = [cluster(parts, seed, tail.count("cluster_wait();") == 2) for seed in range(200)]
+    assert any(runs) and not all(runs)                      # with waits that ran out, and without
+
+
+def test_the_model_sees_a_cta_that_leaves_early():
+    with pytest.raises(AssertionError, match="after its end"):
+        for seed in range(200):
+            cluster(4, seed, False)
+
+
 # ------------------------------------------------------------------ on the GPU
 @pytest.fixture
 def hooks():
@@ -205,14 +262,14 @@ def runs_out(call):
     assert tq.tq4_1s_get_status() & tq.TQ_DEV_TIMEOUT
     assert elapsed < 1.0
     for _ in range(3):
-        assert torch.equal(call().view(torch.int16), want.view(torch.int16))
+        assert torch.equal(call().view(torch.uint8), want.view(torch.uint8))
     assert tq.tq4_1s_get_status() == 0
 
 
-def linear(m, n, k):
+def linear(m, n, k, dtype=torch.bfloat16):
     g = torch.Generator().manual_seed(m + n + k)
     w = tq.tq4_1s_int8_quantize(torch.randn(n, k, generator=g).to(DEV))
-    x = torch.randn(m, k, generator=g).to(torch.bfloat16).to(DEV)
+    x = torch.randn(m, k, generator=g).to(dtype).to(DEV)
     return lambda: tq.tq4_1s_linear_int8(x, w)
 
 
@@ -232,6 +289,14 @@ def moe(m, E, topk, H, I):
 def test_linear_winds_down(hooks, m, n, k):
     # few tokens, many row tiles a block; one tile a block, and several
     runs_out(linear(m, n, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k,dtype", [(1, 4096, 2688, torch.float16), (16, 4096, 4096, torch.bfloat16),
+                                         (5, 300, 9216, torch.float32), (3, 7000, 4096, torch.bfloat16)])
+def test_clusters_wind_down(hooks, m, n, k, dtype):
+    # a row tile's k over 4, 4, 8 and 2 blocks, with stages used again in the last
+    runs_out(linear(m, n, k, dtype))
 
 
 @pytest.mark.gpu
