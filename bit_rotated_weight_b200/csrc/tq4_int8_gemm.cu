@@ -401,6 +401,8 @@ struct PairShared {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
+  int filled[2];                 // stages that each CTA's copies were sent to (the first CTA's memory)
+  int gave_up;                   // in either CTA
   int epi_ok[2];
   alignas(16) float sx[2][kPairTok];
 };
@@ -415,6 +417,18 @@ __device__ __forceinline__ Place place_of_pair(const Int8GemmArgs& a, int32_t ti
   p.ntok = min(kPairTok, a.m - p.tok0);
   half = (p.ntok + 31) / 32 * 16;
   return p;
+}
+
+// Where a wait ran out: waits for both CTAs' copies in flight, whose bytes the
+// first CTA's barriers count.  One of the two may have sent more.
+__device__ __noinline__ void land_pair(PairShared& sh) {
+  const int own = sh.filled[0], other = sh.filled[1], most = max(own, other);
+  for (int i = max(0, most - kPairStages); i < most; ++i) {
+    uint64_t* bar = &sh.full[i % kPairStages];
+    if (i >= own) mbar_arrive_expect_tx(bar, kPairStageBytes);   // the second CTA's alone
+    else if (i >= other) mbar_complete_tx(bar, kPairStageBytes);
+    int8_drain_wait(bar, (i / kPairStages) & 1);
+  }
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&sh.dempty[i], 2 * kPairEpilogue / 32);
     }
     mbar_init(&sh.mma_done, 1);
-    sh.abort_flag = 0;
+    sh.abort_flag = sh.gave_up = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
@@ -490,12 +504,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
       }
-      if (*abortp && rank == 0)   // let the copies in flight land (both CTAs stay until the barrier at the end)
-        for (int i = 0; i < min(li, kPairStages); ++i) {
-          s = s == 0 ? kPairStages - 1 : s - 1;
-          if (s == kPairStages - 1) ph ^= 1u;
-          int8_drain_wait(&sh.full[s], ph);
-        }
+      store_remote(in_cta(&sh.filled[rank], 0), li);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             ph ^= 1u;
           }
         }
-        if (ok && elect_one()) mma_commit_pair(&sh.dfull[db]);
+        if (ok && !(a.test_withhold && ti == 0) && elect_one()) mma_commit_pair(&sh.dfull[db]);
         __syncwarp();
       }
       if (elect_one()) {
@@ -568,9 +577,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abortp)
+    for (int i = 0; i < 2; ++i) store_remote(in_cta(&sh.gave_up, i), 1);
   cluster_arrive();   // neither CTA leaves, or frees its tensor memory, while the other may still reach it
   cluster_wait();
   tc_fence_after();
+  if (sh.gave_up) {   // (the same in both)
+    if (rank == 0 && threadIdx.x == 0) land_pair(sh);
+    cluster_arrive();
+    cluster_wait();
+  }
+  // The MMAs' last arrivals are sent to both CTAs.  The first has seen its own.
+  if (rank == 1 && threadIdx.x == 0) int8_drain_wait(&sh.mma_done, 0);
   if (warp == 2) tmem_dealloc2(tmem, 512);
 }
 

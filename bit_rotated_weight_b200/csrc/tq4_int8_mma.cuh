@@ -104,6 +104,7 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ void int8_drain_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait(addr, parity)) return;   // (the timer takes longer to read)
   const uint64_t t0 = global_timer();
   while (!mbar_try_wait(addr, parity)) {
     if (global_timer() - t0 > TQ_WAIT_NS) {
@@ -111,6 +112,15 @@ __device__ __forceinline__ void int8_drain_wait(uint64_t* bar, uint32_t parity) 
       return;
     }
   }
+}
+
+__device__ __forceinline__ void store_remote(uint32_t at, int32_t v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+// Counts bytes that a barrier expects and that will not come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+               : "memory");
 }
 
 // Waits for a ring's copies in flight: `filled` were sent, the last `stages` of

@@ -236,6 +236,106 @@ def test_the_model_sees_a_cta_that_leaves_early():
             cluster(4, seed, False)
 
 
+# ------------------------------------------------------------------ two CTAs on one tile
+def pair(stages, total, seed, both, last):
+    """The ring of a pair, whose roles give up at random moments (the second CTA's at others).  A copy's bytes and the
+    arrival that expects them are counted by the first CTA; commits arrive at both, at different times.
+    `both`: at the end the first CTA waits for the copies of both, else for those of the stages that it sent itself, if
+    it saw by then that it gave up.  `last`: the second CTA stays for its last arrival."""
+    rng = random.Random(seed)
+    give_up = [rng.randrange(6 * total), rng.randrange(12 * total)]
+    aborted = [False, False]
+    pending, tx = [1] * stages, [0] * stages               # of the first CTA's barriers
+    full = [0] * stages
+    empty = [[0] * stages for _ in range(2)]
+    flying, arrivals = [], []                              # (cta, fill); (cta, stage or "done")
+    sent, producing, issuing, issued = [0, 0], [True, True], True, 0
+    seen = None                                            # what the first producer saw when it ended
+    done = [False, False]
+
+    def settle(s):
+        if pending[s] == 0 and tx[s] == 0:
+            full[s], pending[s] = full[s] + 1, 1
+
+    def land():
+        cta, li = flying.pop(rng.randrange(len(flying)))
+        tx[li % stages] -= 1
+        settle(li % stages)
+
+    def arrive():
+        cta, what = arrivals.pop(rng.randrange(min(2, len(arrivals))))
+        if what == "done":
+            done[cta] = True
+        else:
+            empty[cta][what] += 1
+
+    for event in range(100000):
+        for c in range(2):
+            aborted[c] |= event >= give_up[c]
+        act = rng.randrange(5)
+        if act == 0 and flying and rng.random() < 0.3:
+            land()
+        elif act == 1 and arrivals:
+            arrive()
+        elif act in (2, 3) and producing[act - 2]:
+            c, li = act - 2, sent[act - 2]
+            free = li < stages or empty[c][li % stages] >= li // stages
+            if li == total or (not free and aborted[c]):
+                producing[c] = False
+                if c == 0:
+                    seen = aborted[0]
+            elif free:
+                if c == 0:
+                    pending[li % stages] -= 1
+                    tx[li % stages] += 2
+                    settle(li % stages)
+                flying.append((c, li))
+                sent[c] += 1
+        elif act == 4 and issuing:
+            if issued < total and full[issued % stages] > issued // stages:
+                arrivals += [(0, issued % stages), (1, issued % stages)]
+                issued += 1
+            elif issued == total or aborted[0]:
+                arrivals += [(0, "done"), (1, "done")]
+                issuing = False
+        if not any(producing) and not issuing and done[0] and all(aborted):
+            break                                           # both CTAs are at the cluster barrier
+    else:
+        raise AssertionError("stuck")
+    own, other = sent
+    most = max(own, other) if both else own if seen else 0
+    for i in range(max(0, most - stages), most):
+        s = i % stages
+        if both and i >= own:
+            pending[s] -= 1
+            tx[s] += 1
+            settle(s)
+        elif both and i >= other:
+            tx[s] -= 1
+            settle(s)
+        while full[s] <= i // stages and flying:
+            land()
+        if both:
+            assert full[s] > i // stages
+    while last and not done[1]:
+        arrive()
+    return flying, [a for a in arrivals if a[1] == "done"]
+
+
+@pytest.mark.parametrize("stages,total", [(6, 4), (6, 30), (2, 9)])
+def test_a_pair_ends_with_nothing_on_its_way(stages, total):
+    text = source("tq4_int8_gemm.cu")
+    text = text[text.index("int8_pair_kernel("):text.index("cudaError_t launch_pair")]
+    end = text[text.rindex("__syncthreads();"):]
+    for seed in range(300):
+        assert pair(stages, total, seed, "land_pair(sh)" in end, "int8_drain_wait(&sh.mma_done, 0)" in end) == ([], [])
+
+
+def test_the_model_sees_what_a_pair_leaves_behind():
+    runs = [pair(6, 30, seed, False, False) for seed in range(300)]
+    assert any(flying for flying, _ in runs) and any(late for _, late in runs)
+
+
 # ------------------------------------------------------------------ on the GPU
 @pytest.fixture
 def hooks():
@@ -288,6 +388,12 @@ def moe(m, E, topk, H, I):
                                    (100, 40000, 512)])
 def test_linear_winds_down(hooks, m, n, k):
     # few tokens, many row tiles a block; one tile a block, and several
+    runs_out(linear(m, n, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,k", [(2400, 4360, 416), (5000, 8192, 1024), (2304, 4096, 32)])
+def test_pairs_wind_down(hooks, m, n, k):
     runs_out(linear(m, n, k))
 
 
