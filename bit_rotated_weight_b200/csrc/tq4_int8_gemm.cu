@@ -651,7 +651,7 @@ cudaError_t launch_int8_gemm(const CUtensorMap& tw, const CUtensorMap& tx, const
   switch (nt) {
     case kInt8Pair: return launch_pair(tw, tx, a, grid, st);
     case 16: return launch<16>(tw, tx, a, grid, st);
-    case 32: return launch<32>(tw, tx, a, grid, st);
+    case 32: return launch_as<32, false>(tw, tx, a, grid, st);   // (segments have 16, 64, 128 or 256 rows)
     case 64: return launch<64>(tw, tx, a, grid, st);
     case 128: return launch<128>(tw, tx, a, grid, st);
     default: return launch<256>(tw, tx, a, grid, st);
