@@ -410,3 +410,22 @@ def test_clusters_wind_down(hooks, m, n, k, dtype):
 def test_moe_winds_down(hooks, m, E, topk, H, I):
     # slots sorted in the product, a segment a block; segments from a kernel of their own, several a block; tiles
     runs_out(moe(m, E, topk, H, I))
+
+
+@pytest.mark.gpu
+def test_failed_launches_are_reported_and_launch_nothing(hooks):
+    W, z = torch.randn(64, 96, generator=torch.Generator().manual_seed(1)).to(DEV), torch.randn(5, 8, device=DEV)
+    w = tq.tq4_1s_int8_quantize(W)
+    few, many, pairs = linear(3, 300, 256), linear(40, 300, 256), linear(2304, 4096, 32)
+    experts, prompt = moe(2, 16, 4, 256, 128), moe(300, 8, 2, 512, 288)
+    for call in (lambda: tq.tq4_1s_int8_quantize(W).q, lambda: tq.tq4_1s_int8_dequantize(w), few, many, pairs, experts,
+                 prompt, lambda: tq.tq4_1s_router_scored(z, 2)[1]):
+        want = call()
+        torch.cuda.synchronize()
+        tq.tq4_1s_debug_hook(tq.TQ_HOOK_FAIL_NEXT_CALLS, 1)
+        before = tq.tq4_1s_launch_count()
+        with pytest.raises(tq.TQ4Error) as e:
+            call()
+        assert e.value.code == 5 and tq.tq4_1s_launch_count() == before
+        assert torch.equal(call(), want) and tq.tq4_1s_launch_count() > before
+    assert tq.tq4_1s_get_status() == 0
