@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(Shape<NT>::kThreads, 1)
 // its own 128 rows.  The first CTA's `full` barriers count the bytes of both,
 // its commits free the stages of both, and its `dempty` counts the epilogue
 // warps of both.  Bound by the tensor cores: 8192 x 14336 x 4096 in 286 us, 3.4
-// POP/s, as a burst; 335 to 350 us under the power limit.  (Alone, a CTA's 48 KB a k
-// step took 324 and 385 us.)
+// POP/s, as a burst; 335 to 360 us under the power limit.  (Alone, a CTA's 48 KB a k
+// step took 324 and 385 us.)  The MMAs' last arrival goes to both CTAs, so the
+// second waits for its own too before it leaves.
 constexpr int kPairTok = 256;
 constexpr int kPairStageBytes = kABytes + kPairTok / 2 * kStep;
 constexpr int kPairStages = (200 * 1024) / kPairStageBytes;
